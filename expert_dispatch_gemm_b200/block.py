@@ -1,0 +1,590 @@
+"""Thin Python binding of libmoe_block (include/moe_block.h): the operators of
+the transformer block around the MoE layer, and the layer's experts in 8-bit
+integers.
+
+Argument checking and marshalling only, as in ``moe.py``, whose statuses,
+errors, configs and workspaces it shares; every step runs in the library's CUDA
+kernels on the stream given (default: the tensors' device's current stream). If
+``libmoe_block.so`` is missing every call raises, there is no fallback.
+
+``Block`` runs a layer between its norms, forward and backward, and clips its
+gradients; ``QuantizedLayer`` serves a layer with 8-bit experts.
+"""
+from __future__ import annotations
+
+import bisect
+import ctypes
+import os
+
+import torch
+
+from . import moe
+from .moe import MOE_BF16, MOE_F32, MOE_OK, MoeError, RouteBuffers
+from .workloads import Workload
+
+_PKG = os.path.dirname(os.path.abspath(__file__))
+# MOE_LIBRARY=checked loads the checked build, as for libmoe
+LIB_PATH = os.path.join(_PKG, "libmoe_block_checked.so"
+                        if os.environ.get("MOE_LIBRARY") == "checked" else "libmoe_block.so")
+
+# limits of include/moe_block.h
+MOE_NORM_MAX_D = 16384
+MOE_I8_MAX_GROUPS = 260
+MOE_I8_MAX_K = 65536
+MOE_WS_ERROR_BYTES = 256
+I8_ACTS = {"relu": moe.MOE_ACT_RELU, "gelu": moe.MOE_ACT_GELU, "swiglu": moe.MOE_ACT_SWIGLU,
+           "none": 3}
+
+# every entry point include/moe_block.h declares
+API_SYMBOLS = ["moe_norm_validate", "moe_norm_workspace_size", "moe_norm_forward",
+               "moe_norm_backward", "moe_residual_norm_forward", "moe_residual_norm_backward",
+               "moe_grad_workspace_size", "moe_grad_norm", "moe_grad_clip", "moe_quantize_rows",
+               "moe_gemm_i8_validate", "moe_gemm_i8_workspace_size", "moe_gemm_i8",
+               "moe_dispatch_i8"]
+
+
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("d", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("block_scale", ctypes.c_float),
+                ("gate_tokens", ctypes.c_int), ("gate_stride", ctypes.c_longlong)]
+
+
+class MoeGradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("numel", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+class MoeGemmI8Config(ctypes.Structure):
+    _fields_ = [("groups", ctypes.c_int), ("rows", ctypes.c_int), ("k", ctypes.c_int),
+                ("n_out", ctypes.c_int), ("act", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class MoeDispatchI8Config(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("d", ctypes.c_int), ("E", ctypes.c_int),
+                ("n_shared", ctypes.c_int), ("slots", ctypes.c_int), ("rows", ctypes.c_int),
+                ("shared_row_base", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+_LIB = None
+
+
+def lib() -> ctypes.CDLL:
+    global _LIB
+    if _LIB is None:
+        if not os.path.exists(LIB_PATH):
+            raise RuntimeError(f"{LIB_PATH} is missing: build it with "
+                               "`python -m expert_dispatch_gemm_b200.build`")
+        L = ctypes.CDLL(LIB_PATH)
+        P, size, sizep = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+        ncfg = ctypes.POINTER(MoeNormConfig)
+        gcfg = ctypes.POINTER(MoeGemmI8Config)
+        L.moe_norm_validate.argtypes = [ncfg]
+        L.moe_norm_workspace_size.argtypes = [ncfg, sizep]
+        L.moe_norm_forward.argtypes = [ncfg, P, P, P, P, P]
+        L.moe_norm_backward.argtypes = [ncfg, P, P, P, P, P, P, P, P, size, P]
+        L.moe_residual_norm_forward.argtypes = [ncfg] + [P] * 10
+        L.moe_residual_norm_backward.argtypes = [ncfg] + [P] * 15 + [size, P]
+        L.moe_grad_workspace_size.argtypes = [ctypes.c_int, sizep]
+        tens = ctypes.POINTER(MoeGradTensor)
+        L.moe_grad_norm.argtypes = [tens, ctypes.c_int, P, P, size, P]
+        L.moe_grad_clip.argtypes = [tens, ctypes.c_int, ctypes.c_float, P, P, size, P]
+        L.moe_quantize_rows.argtypes = [ctypes.c_longlong, ctypes.c_int, ctypes.c_int, P, P, P,
+                                        P, P, ctypes.c_int, P]
+        L.moe_gemm_i8_validate.argtypes = [gcfg]
+        L.moe_gemm_i8_workspace_size.argtypes = [gcfg, sizep]
+        L.moe_gemm_i8.argtypes = [gcfg] + [P] * 10 + [size, P]
+        L.moe_dispatch_i8.argtypes = [ctypes.POINTER(MoeDispatchI8Config), P,
+                                      ctypes.POINTER(moe.MoeRouteOut), P, P, P, P, P]
+        for s in API_SYMBOLS:
+            getattr(L, s).restype = ctypes.c_int
+        _LIB = L
+    return _LIB
+
+
+# ---------------------------------------------------------------------------
+# argument checks
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+_TORCH = {MOE_F32: torch.float32, MOE_BF16: torch.bfloat16}
+
+
+def _dtype(dt) -> int:
+    if dt not in _DTYPES:
+        raise TypeError(f"expected float32 or bfloat16, got {dt}")
+    return _DTYPES[dt]
+
+
+class _Args:
+    """Checks the tensors of one call and hands out their addresses; they have
+    to be on one CUDA device."""
+    __slots__ = ("device",)
+
+    def __init__(self, first):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError("expected a CUDA tensor")
+        self.device = first.device
+
+    def __call__(self, t, name, dtype, shape=None, optional=False):
+        if t is None:
+            if optional:
+                return None
+            raise ValueError(f"{name} is missing")
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.device != self.device:
+            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def call(self, what, fn, stream, *args):
+        """fn(*args, stream) on the tensors' device; raises MoeError."""
+        index = self.device.index
+        if stream is None:
+            raw = torch._C._cuda_getCurrentRawStream(index)
+        else:
+            if stream.device != self.device:
+                raise ValueError(f"the stream is of {stream.device}, the tensors are on "
+                                 f"{self.device}")
+            raw = stream.cuda_stream
+        if index == torch.cuda.current_device():
+            status = fn(*args, raw)
+        else:
+            with torch.cuda.device(index):
+                status = fn(*args, raw)
+        if status != MOE_OK:
+            raise MoeError(status, what)
+
+
+def _check(status: int, what: str):
+    if status != MOE_OK:
+        raise MoeError(status, what)
+
+
+def _bytes(device, nbytes: int) -> torch.Tensor:
+    ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + nbytes]
+
+
+def _workspace(a: _Args, ws):
+    return a(ws, "ws", torch.uint8), ws.numel()
+
+
+# ---------------------------------------------------------------------------
+# residual norms
+# ---------------------------------------------------------------------------
+
+def norm_config(n: int, d: int, dtype, eps: float, weight_offset: float = 0.0,
+                res_scale: float = 1.0, block_scale: float = 1.0, gate_tokens: int = 0,
+                gate_stride: int | None = None) -> MoeNormConfig:
+    return MoeNormConfig(n=n, d=d, dtype=_dtype(dtype), eps=eps, weight_offset=weight_offset,
+                         res_scale=res_scale, block_scale=block_scale, gate_tokens=gate_tokens,
+                         gate_stride=d if gate_stride is None else gate_stride)
+
+
+def norm_gate_rows(cfg: MoeNormConfig) -> int:
+    return -(-cfg.n // cfg.gate_tokens) if cfg.gate_tokens else 1
+
+
+def norm_validate(cfg: MoeNormConfig) -> int:
+    return lib().moe_norm_validate(cfg)
+
+
+def norm_workspace(cfg: MoeNormConfig, device) -> torch.Tensor:
+    """Workspace of the backward calls (one call at a time)."""
+    nbytes = ctypes.c_size_t()
+    _check(lib().moe_norm_workspace_size(cfg, ctypes.byref(nbytes)), "moe_norm_workspace_size")
+    return _bytes(device, nbytes.value)
+
+
+def _gate(a: _Args, t, name, cfg, dt):
+    """A gate or its gradient: [rows, d] (or [d] for one row) with unit column
+    stride and cfg.gate_stride between rows."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    rows, d = norm_gate_rows(cfg), cfg.d
+    if t.dtype is not dt:
+        raise TypeError(f"{name}: expected {dt}, got {t.dtype}")
+    if t.device != a.device:
+        raise ValueError(f"{name} is on {t.device}, not on {a.device}")
+    if t.shape != (rows, d) and not (rows == 1 and t.shape == (d,)):
+        raise ValueError(f"{name}: expected shape {(rows, d)}, got {tuple(t.shape)}")
+    if (d > 1 and t.stride(-1) != 1) or (rows > 1 and t.stride(0) != cfg.gate_stride):
+        raise ValueError(f"{name}: strides {t.stride()} are not ({cfg.gate_stride}, 1)")
+    return t.data_ptr()
+
+
+def moe_norm_forward(cfg: MoeNormConfig, x, w, h, rstd=None, stream=None):
+    """h = norm(x): the pre-norm alone."""
+    a, dt, f32 = _Args(x), _TORCH[cfg.dtype], torch.float32
+    n, d = cfg.n, cfg.d
+    a.call("moe_norm_forward", lib().moe_norm_forward, stream, cfg, a(x, "x", dt, (n, d)),
+           a(w, "w", f32, (d,)), a(h, "h", dt, (n, d)), a(rstd, "rstd", f32, (n,), True))
+
+
+def moe_norm_backward(cfg: MoeNormConfig, dres, dh, x, w, rstd, dx, dw, ws, stream=None):
+    """dx = dres + d<dh, norm(x)>/dx and dw (dres may be None)."""
+    a, dt, f32 = _Args(x), _TORCH[cfg.dtype], torch.float32
+    nd, n, d = (cfg.n, cfg.d), (cfg.n,), (cfg.d,)
+    a.call("moe_norm_backward", lib().moe_norm_backward, stream, cfg,
+           a(dres, "dres", dt, nd, True), a(dh, "dh", dt, nd), a(x, "x", dt, nd),
+           a(w, "w", f32, d), a(rstd, "rstd", f32, n), a(dx, "dx", dt, nd), a(dw, "dw", f32, d),
+           *_workspace(a, ws))
+
+
+def moe_residual_norm_forward(cfg: MoeNormConfig, x, y, w_post, gate, w_next, out, h=None,
+                              rstd_post=None, rstd_next=None, stream=None):
+    """out = res_scale x + block_scale gate * norm(y), h = norm(out); w_post,
+    gate, w_next (with h) and the inverse norms may be None."""
+    a, dt, f32 = _Args(x), _TORCH[cfg.dtype], torch.float32
+    nd, n, d = (cfg.n, cfg.d), (cfg.n,), (cfg.d,)
+    a.call("moe_residual_norm_forward", lib().moe_residual_norm_forward, stream, cfg,
+           a(x, "x", dt, nd), a(y, "y", dt, nd), a(w_post, "w_post", f32, d, True),
+           _gate(a, gate, "gate", cfg, dt), a(w_next, "w_next", f32, d, True),
+           a(out, "out", dt, nd), a(h, "h", dt, nd, True),
+           a(rstd_post, "rstd_post", f32, n, True), a(rstd_next, "rstd_next", f32, n, True))
+
+
+def moe_residual_norm_backward(cfg: MoeNormConfig, dout, dh, out, y, w_post, gate, w_next,
+                               rstd_post, rstd_next, dx, dy, dw_post, dgate, dw_next, ws,
+                               stream=None):
+    """Gradients of <dout, out> + <dh, h> (see include/moe_block.h for what may
+    be None)."""
+    a, dt, f32 = _Args(y), _TORCH[cfg.dtype], torch.float32
+    nd, n, d = (cfg.n, cfg.d), (cfg.n,), (cfg.d,)
+    a.call("moe_residual_norm_backward", lib().moe_residual_norm_backward, stream, cfg,
+           a(dout, "dout", dt, nd, True), a(dh, "dh", dt, nd, True),
+           a(out, "out", dt, nd, True), a(y, "y", dt, nd), a(w_post, "w_post", f32, d, True),
+           _gate(a, gate, "gate", cfg, dt), a(w_next, "w_next", f32, d, True),
+           a(rstd_post, "rstd_post", f32, n, True), a(rstd_next, "rstd_next", f32, n, True),
+           a(dx, "dx", dt, nd), a(dy, "dy", dt, nd), a(dw_post, "dw_post", f32, d, True),
+           _gate(a, dgate, "dgate", cfg, dt), a(dw_next, "dw_next", f32, d, True),
+           *_workspace(a, ws))
+
+
+# ---------------------------------------------------------------------------
+# gradient norm and clip
+# ---------------------------------------------------------------------------
+
+class GradList:
+    """The gradients of one moe_grad_norm / moe_grad_clip call, and where the
+    clipped copies go (None: in place). Holds the tensors."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"{len(self.grads)} gradients, {len(self.outs)} outputs")
+        self.count = len(self.grads)
+        self.device = self.grads[0].device if self.grads else None
+        self.c = (MoeGradTensor * max(self.count, 1))()
+        spans = []
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            for t in (g, o):
+                if not isinstance(t, torch.Tensor) or not t.is_cuda:
+                    raise ValueError(f"gradient {i}: expected CUDA tensors")
+                if t.device != self.device:
+                    raise ValueError(f"gradient {i} is on {t.device}, not on {self.device}")
+                if not t.is_contiguous():
+                    raise ValueError(f"gradient {i} must be contiguous")
+            if o.dtype is not g.dtype or o.shape != g.shape:
+                raise ValueError(f"gradient {i}: its output has another dtype or shape")
+            n = g.numel()
+            self.c[i] = MoeGradTensor(g.data_ptr(), o.data_ptr(), n, _dtype(g.dtype))
+            if n:
+                spans.append((o.data_ptr(), o.data_ptr() + n * o.element_size(), i))
+        # what is written may meet nothing but its own gradient, whole
+        spans.sort()
+        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"the outputs of gradients {i} and {j} overlap")
+        firsts = [s[0] for s in spans]
+        for i, g in enumerate(self.grads):
+            a = g.data_ptr()
+            b = a + g.numel() * g.element_size()
+            for s in spans[max(bisect.bisect_right(firsts, a) - 1, 0):
+                           bisect.bisect_left(firsts, b)]:
+                if s[0] < b and a < s[1] and not (s[2] == i and s[:2] == (a, b)):
+                    raise ValueError(f"the output of gradient {s[2]} overlaps gradient {i}")
+
+
+def grad_list(grads, outs=None) -> GradList:
+    return GradList(grads, outs)
+
+
+def grad_workspace(grads: GradList, device) -> torch.Tensor:
+    nbytes = ctypes.c_size_t()
+    _check(lib().moe_grad_workspace_size(grads.count, ctypes.byref(nbytes)),
+           "moe_grad_workspace_size")
+    return _bytes(device, nbytes.value)
+
+
+def _grad_args(grads: GradList, norm, ws, least):
+    a = _Args(norm)
+    if grads.device is not None and grads.device != a.device:
+        raise ValueError(f"norm is on {a.device}, the gradients are on {grads.device}")
+    if norm.numel() < least:
+        raise ValueError(f"norm needs {least} elements")
+    return a, a(norm, "norm", torch.float32), *_workspace(a, ws)
+
+
+def moe_grad_norm(grads: GradList, norm, ws, stream=None):
+    """norm[0] = the L2 norm over all gradients."""
+    a, pn, pw, nw = _grad_args(grads, norm, ws, 1)
+    a.call("moe_grad_norm", lib().moe_grad_norm, stream, grads.c, grads.count, pn, pw, nw)
+
+
+def moe_grad_clip(grads: GradList, max_norm: float, norm, ws, stream=None):
+    """norm[0] = the norm, norm[1] = the factor min(1, max_norm / (norm + 1e-6));
+    the outputs receive the gradients times the factor."""
+    a, pn, pw, nw = _grad_args(grads, norm, ws, 2)
+    a.call("moe_grad_clip", lib().moe_grad_clip, stream, grads.c, grads.count, max_norm, pn, pw,
+           nw)
+
+
+# ---------------------------------------------------------------------------
+# 8-bit experts
+# ---------------------------------------------------------------------------
+
+def gemm_i8_config(groups: int, rows: int, k: int, n_out: int, act: str = "none",
+                   dtype=torch.bfloat16) -> MoeGemmI8Config:
+    if act not in I8_ACTS:
+        raise ValueError(f"unknown activation {act!r}")
+    return MoeGemmI8Config(groups=groups, rows=rows, k=k, n_out=n_out, act=I8_ACTS[act],
+                           dtype=_dtype(dtype))
+
+
+def gemm_i8_validate(cfg: MoeGemmI8Config) -> int:
+    return lib().moe_gemm_i8_validate(cfg)
+
+
+def gemm_i8_workspace(cfg: MoeGemmI8Config, device, stream=None) -> torch.Tensor:
+    """Workspace with a cleared error word (moe.moe_read_error reads it)."""
+    nbytes = ctypes.c_size_t()
+    _check(lib().moe_gemm_i8_workspace_size(cfg, ctypes.byref(nbytes)),
+           "moe_gemm_i8_workspace_size")
+    ws = _bytes(device, nbytes.value)
+    with torch.cuda.device(ws.device):
+        _check(moe.lib().moe_workspace_init(moe._ptr(ws), moe._stream(stream)),
+               "moe_workspace_init")
+    return ws
+
+
+def _groups(a: _Args, starts, counts):
+    if (starts is None) != (counts is None):
+        raise ValueError("starts and counts come together")
+    if starts is None:
+        return None, None, 0
+    n = starts.numel()
+    return (a(starts, "starts", torch.int32, (n,)), a(counts, "counts", torch.int32, (n,)), n)
+
+
+def moe_quantize_rows(x, q, scale, starts=None, counts=None, stream=None):
+    """q, scale = the rows of x [..., cols] in 8 bits with a scale each; with
+    starts / counts only the groups' rows are read and written."""
+    a = _Args(x)
+    if x.dim() < 1:
+        raise ValueError("x needs at least one dimension")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    px, pq = a(x, "x", x.dtype), a(q, "q", torch.int8, x.shape)
+    ps = a(scale, "scale", torch.float32, x.shape[:-1])
+    p0, p1, groups = _groups(a, starts, counts)
+    a.call("moe_quantize_rows", lib().moe_quantize_rows, stream, rows, cols, _dtype(x.dtype), px,
+           pq, ps, p0, p1, groups)
+
+
+def moe_gemm_i8(cfg: MoeGemmI8Config, xq, x_scale, starts, counts, w, w_scale, w3, w3_scale, out,
+                ws, stream=None):
+    """out = act of the grouped 8-bit products (w3 / w3_scale only for SwiGLU;
+    starts and counts None: one group of all rows)."""
+    a, i8, f32 = _Args(xq), torch.int8, torch.float32
+    g, rows, k, o = cfg.groups, cfg.rows, cfg.k, cfg.n_out
+    p0, p1, n = _groups(a, starts, counts)
+    if starts is not None and n != g:
+        raise ValueError(f"starts and counts have {n} groups, the config {g}")
+    wshape, sshape = (g, o, k), (g, o)
+    a.call("moe_gemm_i8", lib().moe_gemm_i8, stream, cfg, a(xq, "xq", i8, (rows, k)),
+           a(x_scale, "x_scale", f32, (rows,)), p0, p1, a(w, "w", i8, wshape),
+           a(w_scale, "w_scale", f32, sshape), a(w3, "w3", i8, wshape, True),
+           a(w3_scale, "w3_scale", f32, sshape, True), a(out, "out", _TORCH[cfg.dtype], (rows, o)),
+           *_workspace(a, ws))
+
+
+def dispatch_i8_config(cfg: moe.MoeConfig) -> MoeDispatchI8Config:
+    """The dispatch of a layer config (sizes from moe_sizes)."""
+    sz = moe.sizes(cfg)
+    return MoeDispatchI8Config(n=cfg.n, d=cfg.d, E=cfg.E, n_shared=cfg.n_shared, slots=sz.slots,
+                               rows=sz.rows, shared_row_base=sz.shared_row_base, dtype=cfg.dtype)
+
+
+def moe_dispatch_i8(cfg: MoeDispatchI8Config, X, route: RouteBuffers, q, scale, starts, counts,
+                    stream=None):
+    """Each token quantised once and written to its dispatched rows (and its
+    shared-expert rows); starts / counts = the groups of moe_gemm_i8."""
+    a = _Args(X)
+    g = cfg.E + cfg.n_shared
+    for name, shape in (("tok_row", (cfg.n, cfg.slots)), ("offsets", (cfg.E + 1,)),
+                        ("counts", (cfg.E,))):
+        a(getattr(route, name), "route." + name, torch.int32, shape)
+    a.call("moe_dispatch_i8", lib().moe_dispatch_i8, stream, cfg,
+           a(X, "X", _TORCH[cfg.dtype], (cfg.n, cfg.d)), ctypes.byref(route.c),
+           a(q, "q", torch.int8, (cfg.rows, cfg.d)), a(scale, "scale", torch.float32, (cfg.rows,)),
+           a(starts, "starts", torch.int32, (g,)), a(counts, "counts", torch.int32, (g,)))
+
+
+# ---------------------------------------------------------------------------
+# a layer with 8-bit experts, and a block
+# ---------------------------------------------------------------------------
+
+def quantize_weights(w, shared=None):
+    """Expert weights [E, out, in] (and shared experts' [s, out, in], behind
+    them) in 8 bits with a scale for each output channel."""
+    total = w.shape[0] + (0 if shared is None else shared.shape[0])
+    q = torch.empty((total, *w.shape[1:]), dtype=torch.int8, device=w.device)
+    s = torch.empty((total, w.shape[1]), dtype=torch.float32, device=w.device)
+    moe_quantize_rows(w, q[:w.shape[0]], s[:w.shape[0]])
+    if shared is not None:
+        moe_quantize_rows(shared, q[w.shape[0]:], s[w.shape[0]:])
+    return q, s
+
+
+class QuantizedLayer:
+    """A layer for serving with its experts (routed and shared) in 8-bit
+    integers: moe_route, moe_dispatch_i8, the up product with the activation,
+    moe_quantize_rows on the hidden rows, the down product, moe_combine.
+    The router stays in fp32. `inputs` as for moe.Layer; the expert weights are
+    quantised here and not kept."""
+
+    def __init__(self, w: Workload, inputs: dict, device, **cfg_override):
+        self.w = w
+        self.cfg = cfg = moe.config(w, **cfg_override)
+        self.Wg, self.logit_bias = inputs["Wg"], inputs.get("logit_bias")
+        self.sel_bias = inputs.get("sel_bias")
+        self.W1, self.s1 = quantize_weights(inputs["W1"], inputs.get("sW1"))
+        self.W2, self.s2 = quantize_weights(inputs["W2"], inputs.get("sW2"))
+        self.W3, self.s3 = (quantize_weights(inputs["W3"], inputs.get("sW3"))
+                            if w.act == "swiglu" else (None, None))
+        self.route = RouteBuffers(cfg, device)
+        self.ws = moe.workspace(cfg, device, layer=False)
+        sz, dt, g = self.route.sizes, w.torch_dtype, cfg.E + cfg.n_shared
+        self.dispatch_cfg = dispatch_i8_config(cfg)
+        self.up = gemm_i8_config(g, sz.rows, cfg.d, cfg.h, w.act, dt)
+        self.down = gemm_i8_config(g, sz.rows, cfg.h, cfg.d, "none", dt)
+        f32, i32, i8 = torch.float32, torch.int32, torch.int8
+        self.Xq = torch.empty((sz.rows, cfg.d), dtype=i8, device=device)
+        self.xs = torch.empty(sz.rows, dtype=f32, device=device)
+        self.starts = torch.empty(g, dtype=i32, device=device)
+        self.counts = torch.empty(g, dtype=i32, device=device)
+        self.H = torch.empty((sz.rows, cfg.h), dtype=dt, device=device)
+        self.Hq = torch.empty((sz.rows, cfg.h), dtype=i8, device=device)
+        self.hs = torch.empty(sz.rows, dtype=f32, device=device)
+        self.Y = torch.empty((sz.rows, cfg.d), dtype=dt, device=device)
+        self.out = torch.empty((w.n, w.d), dtype=dt, device=device)
+
+    def forward(self, X, stream=None):
+        moe.moe_route(self.cfg, X, self.Wg, self.logit_bias, self.sel_bias, self.route, self.ws,
+                      stream)
+        moe_dispatch_i8(self.dispatch_cfg, X, self.route, self.Xq, self.xs, self.starts,
+                        self.counts, stream)
+        # the products share the routing workspace's error word
+        moe_gemm_i8(self.up, self.Xq, self.xs, self.starts, self.counts, self.W1, self.s1,
+                    self.W3, self.s3, self.H, self.ws, stream)
+        moe_quantize_rows(self.H, self.Hq, self.hs, self.starts, self.counts, stream)
+        moe_gemm_i8(self.down, self.Hq, self.hs, self.starts, self.counts, self.W2, self.s2,
+                    None, None, self.Y, self.ws, stream)
+        moe.moe_combine(self.cfg, self.Y, self.route, self.out, stream)
+        return self.out
+
+
+class Block:
+    """A layer between its norms:
+
+        h = norm(x; w_pre)                    pre-norm
+        y = layer(h)                          moe.Layer (or QuantizedLayer: no backward)
+        out = a x + b gate * norm(y; w_post)  residual norm
+        h_next = norm(out; w_next)            the next block's pre-norm, fused
+
+    params: fp32 "w_pre" [d], and optionally "w_post" [d], "gate" (rows of the
+    layer's dtype, see norm_config) and "w_next" [d]."""
+
+    def __init__(self, layer, params: dict, eps: float = 1e-6, **norm):
+        self.layer, self.p = layer, params
+        w = layer.w
+        self.cfg = norm_config(w.n, w.d, w.torch_dtype, eps, **norm)
+        x = dict(dtype=w.torch_dtype, device=params["w_pre"].device)
+        f = dict(dtype=torch.float32, device=x["device"])
+        self.h, self.out = torch.empty((w.n, w.d), **x), torch.empty((w.n, w.d), **x)
+        self.h_next = torch.empty((w.n, w.d), **x) if params.get("w_next") is not None else None
+        self.r_pre, self.r_post, self.r_next = (torch.empty(w.n, **f) for _ in range(3))
+        self._g = None
+
+    def _tail(self, y, stream):
+        p = self.p
+        moe_residual_norm_forward(self.cfg, self.x, y, p.get("w_post"), p.get("gate"),
+                                  p.get("w_next"), self.out, self.h_next,
+                                  self.r_post if p.get("w_post") is not None else None,
+                                  self.r_next if p.get("w_next") is not None else None, stream)
+        return self.out, self.h_next
+
+    def forward(self, x, stream=None, train=False):
+        """(out, h_next). With train, the layer keeps what its backward needs."""
+        self.x = x
+        moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)
+        run = self.layer.forward_train if train else self.layer.forward
+        return self._tail(run(self.h, stream=stream), stream)
+
+    def forward_train(self, x, stream=None):
+        return self.forward(x, stream, train=True)
+
+    def grads(self):
+        """Gradient buffers (allocated once): "dx", the norms' and the gate's,
+        and the layer's own."""
+        if self._g is None:
+            p, g = self.p, {"dx": torch.empty_like(self.out), "dy": torch.empty_like(self.out),
+                            "dw_pre": torch.empty_like(self.p["w_pre"])}
+            for k in ("w_post", "gate", "w_next"):
+                g["d" + k] = None if p.get(k) is None else torch.empty_like(p[k])
+            self._nws = norm_workspace(self.cfg, self.out.device)
+            g["layer"] = self.layer.grads()
+            self._g = g
+        return self._g
+
+    def backward_train(self, dout, dh_next=None, stream=None):
+        """Gradients of <dout, out> + <dh_next, h_next> after forward_train()."""
+        p, g = self.p, self.grads()
+        r_post = self.r_post if p.get("w_post") is not None else None
+        r_next = self.r_next if p.get("w_next") is not None else None
+        if p.get("w_next") is not None and dh_next is None:
+            raise ValueError("dh_next is missing")
+        moe_residual_norm_backward(self.cfg, dout, dh_next, self.out, self.layer.out,
+                                   p.get("w_post"), p.get("gate"), p.get("w_next"), r_post,
+                                   r_next, g["dx"], g["dy"], g["dw_post"], g["dgate"],
+                                   g["dw_next"], self._nws, stream)
+        lg = self.layer.backward_train(g["dy"], X=self.h, stream=stream)
+        moe_norm_backward(self.cfg, g["dx"], lg["dX"], self.x, p["w_pre"], self.r_pre, g["dx"],
+                          g["dw_pre"], self._nws, stream)
+        return g
+
+    def clip_grads(self, max_norm: float, stream=None):
+        """Scales the parameters' gradients in place so that their global norm
+        is at most max_norm; returns the device tensor [norm, factor]."""
+        if not hasattr(self, "_clip"):
+            g = self.grads()
+            own = [g[k] for k in ("dw_pre", "dw_post", "dgate", "dw_next")]
+            own += [t for k, t in g["layer"].items() if k not in ("dX", "dL")]
+            glist = grad_list([t for t in own if t is not None])
+            self._clip = (glist, torch.empty(2, dtype=torch.float32, device=self.out.device),
+                          grad_workspace(glist, self.out.device))
+        glist, norm, ws = self._clip
+        moe_grad_clip(glist, max_norm, norm, ws, stream)
+        return norm

@@ -3,10 +3,11 @@
     python -m expert_dispatch_gemm_b200.build [--force] [--verbose-ptxas]
 
 Objects go to expert_dispatch_gemm_b200/_build/, the shared library to
-expert_dispatch_gemm_b200/libmoe.so. The checked build of the same sources
+expert_dispatch_gemm_b200/libmoe.so. The operators of the block around the
+layer (include/moe_block.h) go to libmoe_block.so beside it. The checked build of the same sources
 (-DMOE_DEBUG_CHECKS: every out-of-range index read from the routing outputs is
-reported as kErrBadIndex in the error word) goes to libmoe_checked.so, its
-objects to _build_checked/. The FP32 FFMA throughput probe that the benchmark
+reported as kErrBadIndex in the error word) goes to libmoe_checked.so and
+libmoe_block_checked.so, its objects to _build_checked/. The FP32 FFMA throughput probe that the benchmark
 uses for the router's roof goes to libmoe_probe.so. No GPU is needed to
 build.
 """
@@ -27,9 +28,12 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["api.cu", "router.cu", "assign.cu", "dispatch_combine.cu", "ffn_f32.cu",
            "gemm_tc.cu", "gemm_swap.cu", "route_noalloc.cu", "gemm_bwd.cu", "bwd.cu",
            "bwd_f32.cu"]
+BLOCK_SOURCES = ["block_norm.cu", "grad_clip.cu", "quant_i8.cu", "gemm_i8.cu"]
+BLOCK_LIB = os.path.join(PKG, "libmoe_block.so")
 PROBE_SOURCES = ["probe.cu"]
 PROBE_LIB = os.path.join(PKG, "libmoe_probe.so")
 CHECKED_LIB = os.path.join(PKG, "libmoe_checked.so")
+BLOCK_CHECKED_LIB = os.path.join(PKG, "libmoe_block_checked.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -40,7 +44,7 @@ def nvcc() -> str:
 
 
 def _headers():
-    hs = [os.path.join(INCLUDE, "moe.h")]
+    hs = [os.path.join(INCLUDE, f) for f in ("moe.h", "moe_block.h")]
     hs += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     return hs
 
@@ -53,8 +57,11 @@ def _flags(extra=()):
 
 def build(force: bool = False, ptxas_verbose: bool = False, checked: bool = True) -> str:
     lib = _build_lib(SOURCES, LIB, force, ptxas_verbose)
+    _build_lib(BLOCK_SOURCES, BLOCK_LIB, force, ptxas_verbose)
     _build_lib(PROBE_SOURCES, PROBE_LIB, force, ptxas_verbose)
     if checked:
+        _build_lib(BLOCK_SOURCES, BLOCK_CHECKED_LIB, force, False, BUILD_CHECKED,
+                   ["-DMOE_DEBUG_CHECKS"])
         _build_lib(SOURCES, CHECKED_LIB, force, False, BUILD_CHECKED, ["-DMOE_DEBUG_CHECKS"])
     return lib
 

@@ -69,6 +69,7 @@ enum : int {
   kSiteGemmGatherToken = 0x12,
   kSiteGemmScatterToken = 0x13,
   kSiteSwapOffsets = 0x20,
+  kSiteI8Groups = 0x21,
   kSiteScatterIdx = 0x30,
   kSiteEcFinishIdx = 0x31,
   kSiteBwdTokRow = 0x40,

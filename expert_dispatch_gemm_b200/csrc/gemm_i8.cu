@@ -1,0 +1,715 @@
+// Grouped products in 8-bit integers on the tensor cores, with a scale for
+// each token and each output channel:
+//
+//   u[r,o] = x_scale[r] w_scale[g,o] sum_j xq[r,j] w[g,o,j]
+//   out    = act(u), or silu(u) v (SwiGLU, v from a second weight)
+//
+// "Expert choice routing" (aicassindra.com), "The math": Expert_e on dense
+// per-expert batches. The weights are the M side, as in the bf16 weights-as-M
+// products: a group's tokens are the N side of the MMA and need no padding to
+// 128 rows, so the same kernel serves one decoded token (where it streams the
+// active experts' weights once, half the bytes of bf16) and long prompts. An
+// accumulator lane is an output channel and its columns are tokens: the
+// channel's scale is a register, the tokens' scales are read from shared
+// memory, and the int32 sums (exact: |q| <= 127 and K <= 65,536) become fp32
+// once, in the epilogue.
+//
+// CTA pairs (cta_group::2), tcgen05.mma kind::i8, K = 32 a step. A tile is
+// (group, 256 channels, up to 256 of the group's rows): each CTA loads its 128
+// channels as A and half of the rows as B by TMA, 128 bytes of K a stage
+// (128-byte swizzle); K past the end and rows past the buffers arrive as
+// zeros. A step of 32 bytes takes N / 2 cycles of the tensor pipe, as a bf16
+// step of 16 elements does, and one thread issues a step in about 95 cycles,
+// so two threads issue, on accumulators of their own:
+// - i8_pair_kernel: two tile streams, each with its own producer, ring and
+//   256-column accumulator; while one stream's epilogue drains, the other
+//   keeps the pipe busy.
+//     warps 0 / 2 producers, 1 / 3 issuers, 4-11 epilogue (four a stream)
+// - i8_swiglu_pair_kernel: one stream, W1 and W3 rows as two A operands of a
+//   stage, u and v into two accumulators that meet in one epilogue thread.
+//     warp 0 producer, 1 / 2 issuers, 4-11 epilogue
+// Every mbarrier wait is bounded; on a timeout a role records the error, its
+// copies and MMAs in flight are waited for (bounded), TMEM is freed and the
+// kernel returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include <atomic>
+
+#include "block_internal.h"
+#include "device_common.cuh"
+#include "sm100.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kBK = 128;                    // bytes (= elements) of K a stage
+constexpr int kStep = 32;                   // K of one MMA
+constexpr int kWBytes = 128 * kBK;          // this CTA's 128 channels
+constexpr int kXBytes = 128 * kBK;          // up to 128 rows
+constexpr int kMaxTok = 256;                // rows of a tile (MMA N)
+constexpr int kTokUnit = 32;                // N is a multiple of this (M = 256 pairs)
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (4 + kEpiWarps);
+constexpr int kTmemCols = 512;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
+
+constexpr int kStreams = 2, kStagesS = 3, kStageBytesS = kWBytes + kXBytes;  // 3 x 32 KB each
+constexpr int kStagesU = 4, kStageBytesU = 2 * kWBytes + kXBytes;            // 4 x 48 KB
+
+enum { A_NONE = MOE_I8_NONE, A_RELU = MOE_I8_RELU, A_GELU = MOE_I8_GELU };
+
+struct I8Params {
+  const int32_t *starts, *counts;  // NULL: one group of all rows
+  const float *x_scale, *w_scale, *w3_scale;
+  int groups, rows, K, n_out, mt_tiles;
+  void* out;
+  int* err;
+};
+
+struct GroupTable {
+  int start[MOE_I8_MAX_GROUPS];
+  int count[MOE_I8_MAX_GROUPS];
+  int tiles[MOE_I8_MAX_GROUPS + 1];  // tiles of the groups before g
+};
+
+struct StreamState {
+  uint64_t full[kStreams][kStagesS];
+  uint64_t empty[kStreams][kStagesS];
+  uint64_t tfull[kStreams];
+  uint64_t tempty[kStreams];
+  uint64_t drain[kStreams];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  GroupTable g;
+};
+
+struct UpState {
+  uint64_t full[kStagesU];
+  uint64_t empty[kStagesU];  // released by both issuers' commits
+  uint64_t tfull;            // both issuers' last commits of a tile
+  uint64_t tempty;           // both CTAs' epilogues
+  uint64_t drain[2];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  GroupTable g;
+};
+
+template <bool CLUSTER, class State>
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, State* st, int* err,
+                                     int code) {
+  auto probe = [&]() {
+    return CLUSTER ? sm100::mbar_try_wait_cluster(bar, parity) : sm100::mbar_try_wait(bar, parity);
+  };
+  if (probe()) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (probe()) return true;
+    if ((it & 63u) == 0) {
+      if (st->abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitNs) {
+        st->abort_flag = 1;
+        report_error(err, code);
+        return false;
+      }
+    }
+  }
+}
+
+// wait (bounded) for the copies of the last `pending` stages before `stage`
+template <int STAGES>
+__device__ __forceinline__ void settle(uint64_t* full, int stage, uint32_t phase, int pending) {
+  for (int i = 0; i < pending; ++i) {
+    if (--stage < 0) {
+      stage = STAGES - 1;
+      phase ^= 1u;
+    }
+    const uint64_t t0 = global_timer_ns();
+    while (!sm100::mbar_try_wait(&full[stage], phase) && global_timer_ns() - t0 < kWaitNs) {
+    }
+  }
+}
+
+// Groups into shared memory, cut to the rows that the buffers have.
+__device__ __forceinline__ void load_groups(GroupTable& g, const I8Params& p, int tid) {
+  for (int i = tid; i < p.groups; i += kThreads) {
+    const int s = p.starts ? p.starts[i] : 0;
+    const int c = p.starts ? p.counts[i] : p.rows;
+    const int room = s < 0 || s > p.rows ? 0 : p.rows - s;
+    if (s < 0 || c < 0 || c > room) bad_index(p.err, kSiteI8Groups);
+    g.start[i] = s;
+    g.count[i] = max(0, min(c, room));
+  }
+  __syncthreads();
+  if (tid < 32) {  // running sum of the tiles, 32 groups at a time
+    int run = 0;
+    for (int g0 = 0; g0 < p.groups; g0 += 32) {
+      const int i = g0 + tid;
+      int v = i < p.groups ? (g.count[i] + kMaxTok - 1) / kMaxTok * p.mt_tiles : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(~0u, v, o);
+        if (tid >= o) v += u;
+      }
+      if (i < p.groups) g.tiles[i + 1] = run + v;
+      run += __shfl_sync(~0u, v, 31);
+    }
+    if (tid == 0) g.tiles[0] = 0;
+  }
+}
+
+struct Tile {
+  int group, m0;  // first channel of the pair within the group
+  int row;        // first row
+  int valid;      // rows
+  int n;          // MMA N: valid rounded up to kTokUnit
+};
+
+// Tile order: group by group, 256 channels by 256, the rows' chunks innermost
+// (pairs that run together share a weight tile). A group's rows are split
+// into ceil(count / 256) chunks of equal size (rounded up to 32).
+__device__ __forceinline__ Tile decode(int tile, const I8Params& p, const GroupTable& g) {
+  int lo = 0, hi = p.groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (g.tiles[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  Tile t;
+  const int count = g.count[lo];
+  const int chunks = max((count + kMaxTok - 1) / kMaxTok, 1);
+  const int local = tile - g.tiles[lo];
+  const int chunk = local % chunks;
+  const int size = ((count + chunks - 1) / chunks + kTokUnit - 1) / kTokUnit * kTokUnit;
+  t.group = lo;
+  t.m0 = local / chunks * 256;
+  t.row = g.start[lo] + chunk * size;
+  t.valid = min(size, count - chunk * size);
+  t.n = (t.valid + kTokUnit - 1) / kTokUnit * kTokUnit;
+  return t;
+}
+
+// A CTA's rows of the tile (N / 2, a multiple of 16): boxes of 128, 64, 32 and
+// 16 rows at 1 KB-aligned offsets, whole 8-row atoms of the swizzle.
+constexpr int kBoxes = 4;
+struct RowMaps {
+  CUtensorMap m[kBoxes];  // box of 16 << b rows
+};
+__device__ __forceinline__ void load_rows(unsigned char* dst, const RowMaps& x, uint32_t bar,
+                                          int k, int row, int rows) {
+  int off = 0;
+#pragma unroll
+  for (int b = kBoxes - 1; b >= 0; --b) {
+    if (rows & (16 << b)) {
+      sm100::tma_load_2d_pair(dst + off * kBK, &x.m[b], bar, k, row + off);
+      off += 16 << b;
+    }
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  if (ACT == A_RELU) return v < 0.0f ? 0.0f : v;
+  if (ACT == A_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  return v;
+}
+// (bf16 outputs take the fast exponential: its error is far below their step)
+template <typename OUT>
+__device__ __forceinline__ float silu_times(float u, float v) {
+  const float e = sizeof(OUT) == 2 ? __expf(-u) : expf(-u);
+  return u * __frcp_rn(1.0f + e) * v;
+}
+
+// Epilogue staging of a warp, [32 rows][32 channels] bf16: the tile leaves as
+// 16-byte stores of each row's 32 channels. fp32 outputs are not staged (the
+// ring leaves no room): the 32 lanes write a row's 128 consecutive bytes.
+struct Staging {
+  __nv_bfloat16 v[32][32];
+};
+
+// 32 rows from column cc of the tile on: value(i, x_scale of row i) for each
+template <typename OUT, class F>
+__device__ __forceinline__ void emit(Staging* stg, const I8Params& p, const Tile& t, int cc,
+                                     int col0, int lane, const F& value) {
+  const float mine = cc + lane < t.valid ? p.x_scale[t.row + cc + lane] : 0.0f;
+  OUT* out = static_cast<OUT*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
+  sm100::tmem_ld_wait();
+  if constexpr (sizeof(OUT) == 4) {
+    const bool real = col0 + lane < p.n_out;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float r = value(i, __shfl_sync(~0u, mine, i));
+      if (real && cc + i < t.valid) out[(size_t)i * p.n_out + lane] = r;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      stg->v[i][lane] = __float2bfloat16_rn(value(i, __shfl_sync(~0u, mine, i)));
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int idx = k * 32 + lane, i = idx >> 2, c = (idx & 3) * 8;
+      if (cc + i < t.valid && col0 + c < p.n_out)
+        *reinterpret_cast<uint4*>(out + (size_t)i * p.n_out + c) =
+            *reinterpret_cast<const uint4*>(&stg->v[i][c]);
+    }
+    __syncwarp();
+  }
+}
+
+template <typename OUT, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    i8_pair_kernel(const __grid_constant__ RowMaps tx, const __grid_constant__ CUtensorMap tw,
+                   const I8Params p) {
+  extern __shared__ __align__(1024) unsigned char ism[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(ism) + 1023) & ~uintptr_t(1023));
+  constexpr int kRing = kStreams * kStagesS * kStageBytesS;
+  StreamState* st = reinterpret_cast<StreamState*>(base + kRing);
+  Staging* staging = reinterpret_cast<Staging*>(
+      base + kRing + ((sizeof(StreamState) + 127) & ~size_t(127)));
+  auto sW = [&](int sx, int j) { return base + (sx * kStagesS + j) * kStageBytesS; };
+  auto sX = [&](int sx, int j) { return sW(sx, j) + kWBytes; };
+
+  const uint32_t rank = sm100::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int sx = 0; sx < kStreams; ++sx) {
+      for (int j = 0; j < kStagesS; ++j) {
+        sm100::mbar_init(&st->full[sx][j], 1);
+        sm100::mbar_init(&st->empty[sx][j], 1);
+      }
+      sm100::mbar_init(&st->tfull[sx], 1);
+      sm100::mbar_init(&st->tempty[sx], 2 * 32 * (kEpiWarps / kStreams));
+      sm100::mbar_init(&st->drain[sx], 1);
+    }
+    st->abort_flag = 0;
+    sm100::fence_mbar_init();
+  }
+  if (warp == 1) {
+    sm100::tmem_alloc_pair(&st->tmem_base, kTmemCols);
+    sm100::tmem_relinquish_pair();
+  }
+  pdl_wait();
+  load_groups(st->g, p, tid);
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::cluster_sync();  // both CTAs' barriers exist before any remote arrive
+  sm100::tc_fence_after();
+  const uint32_t tmem = st->tmem_base;
+
+  const int total = st->g.tiles[p.groups];
+  const int KB = (p.K + kBK - 1) / kBK;
+  const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+  // the pair's tiles are pair_id + i * num_pairs; stream sx takes i = sx, sx + 2, ...
+  const int sx = warp < 4 ? (warp >> 1) : (warp - 4) / (kEpiWarps / kStreams);
+  const int first = pair_id + sx * num_pairs, step = kStreams * num_pairs;
+
+  if (warp < 4 && (warp & 1) == 0) {
+    if (lane == 0) {  // producer of stream sx
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = first; ok && tile < total; tile += step) {
+        const Tile t = decode(tile, p, st->g);
+        const int half = t.n / 2;
+        const uint32_t bytes = kWBytes + (uint32_t)half * kBK;
+        const int wrow = t.group * p.n_out + t.m0 + (int)rank * 128;
+        const int xrow = t.row + (int)rank * half;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait<false>(&st->empty[sx][stage], phase ^ 1u, st, p.err, kErrGemmTimeout | 0x61)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fl = sm100::mapa_shared(sm100::smem_addr(&st->full[sx][stage]), 0);
+          if (leader) sm100::mbar_arrive_expect_tx(&st->full[sx][stage], 2 * bytes);
+          sm100::tma_load_2d_pair(sW(sx, stage), &tw, fl, kb * kBK, wrow);
+          load_rows(sX(sx, stage), tx, fl, kb * kBK, xrow, half);
+          ++issued;
+          if (++stage == kStagesS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader) settle<kStagesS>(st->full[sx], stage, phase, min(issued, kStagesS));
+    }
+  } else if (warp < 4) {
+    if (lane == 0 && leader) {  // issuer of stream sx
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const uint32_t d_tmem = tmem + (uint32_t)(sx * 256);
+      for (int tile = first; ok && tile < total; tile += step, ++local) {
+        const Tile t = decode(tile, p, st->g);
+        if (!wait<true>(&st->tempty[sx], ((uint32_t)local & 1u) ^ 1u, st, p.err,
+                        kErrGemmTimeout | 0x62)) {
+          ok = false;
+          break;
+        }
+        sm100::tc_fence_after();
+        const uint32_t idesc = sm100::idesc_i8_s32(256, t.n);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait<false>(&st->full[sx][stage], phase, st, p.err, kErrGemmTimeout | 0x63)) {
+            ok = false;
+            break;
+          }
+          sm100::tc_fence_after();
+          const uint64_t da = sm100::sw128_kmajor_desc(sm100::smem_addr(sW(sx, stage)));
+          const uint64_t db = sm100::sw128_kmajor_desc(sm100::smem_addr(sX(sx, stage)));
+#pragma unroll
+          for (int k = 0; k < kBK / kStep; ++k)
+            sm100::umma_i8_pair(d_tmem, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0);
+          sm100::umma_commit_pair_mc(&st->empty[sx][stage], 0x3);
+          if (++stage == kStagesS) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        sm100::umma_commit_pair_mc(&st->tfull[sx], 0x3);
+      }
+      sm100::umma_commit_pair_mc(&st->drain[sx], 0x1);
+      const uint64_t t0 = global_timer_ns();
+      while (!sm100::mbar_try_wait(&st->drain[sx], 0) && global_timer_ns() - t0 < kWaitNs) {
+      }
+    }
+  } else {
+    // epilogue of stream sx: warp q = warp % 4 owns lanes (channels) 32q..32q+31
+    // and walks the tile's rows, 32 at a time
+    const int q = warp & 3;
+    int local = 0;
+    for (int tile = first; tile < total; tile += step, ++local) {
+      const Tile t = decode(tile, p, st->g);
+      const int col0 = t.m0 + (int)rank * 128 + 32 * q;
+      const float ws =
+          col0 + lane < p.n_out ? p.w_scale[(size_t)t.group * p.n_out + col0 + lane] : 0.0f;
+      if (!wait<true>(&st->tfull[sx], (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x64))
+        break;
+      sm100::tc_fence_after();
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(sx * 256);
+#pragma unroll 1
+      for (int cc = 0; cc < t.n; cc += 32) {
+        uint32_t v[32];
+        sm100::tmem_ld_32x32b_x32(tbase + cc, v);
+        emit<OUT>(&staging[warp - 4], p, t, cc, col0, lane, [&](int i, float xs) {
+          return activate<ACT>((float)(int)v[i] * (xs * ws));
+        });
+      }
+      sm100::tc_fence_before();
+      sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty[sx]), 0));
+    }
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+template <typename OUT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    i8_swiglu_pair_kernel(const __grid_constant__ RowMaps tx,
+                          const __grid_constant__ CUtensorMap tw,
+                          const __grid_constant__ CUtensorMap tw3, const I8Params p) {
+  extern __shared__ __align__(1024) unsigned char ism[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(ism) + 1023) & ~uintptr_t(1023));
+  constexpr int kRing = kStagesU * kStageBytesU;
+  UpState* st = reinterpret_cast<UpState*>(base + kRing);
+  Staging* staging = reinterpret_cast<Staging*>(
+      base + kRing + ((sizeof(UpState) + 127) & ~size_t(127)));
+  auto sW = [&](int j, int which) { return base + j * kStageBytesU + which * kWBytes; };
+  auto sX = [&](int j) { return base + j * kStageBytesU + 2 * kWBytes; };
+
+  const uint32_t rank = sm100::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int j = 0; j < kStagesU; ++j) {
+      sm100::mbar_init(&st->full[j], 1);
+      sm100::mbar_init(&st->empty[j], 2);
+    }
+    sm100::mbar_init(&st->tfull, 2);
+    sm100::mbar_init(&st->tempty, 2 * 32 * kEpiWarps);
+    sm100::mbar_init(&st->drain[0], 1);
+    sm100::mbar_init(&st->drain[1], 1);
+    st->abort_flag = 0;
+    sm100::fence_mbar_init();
+  }
+  if (warp == 1) {
+    sm100::tmem_alloc_pair(&st->tmem_base, kTmemCols);
+    sm100::tmem_relinquish_pair();
+  }
+  pdl_wait();
+  load_groups(st->g, p, tid);
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::cluster_sync();
+  sm100::tc_fence_after();
+  const uint32_t tmem = st->tmem_base;
+
+  const int total = st->g.tiles[p.groups];
+  const int KB = (p.K + kBK - 1) / kBK;
+  const int pair_id = blockIdx.x >> 1, num_pairs = gridDim.x >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = pair_id; ok && tile < total; tile += num_pairs) {
+        const Tile t = decode(tile, p, st->g);
+        const int half = t.n / 2;
+        const uint32_t bytes = 2 * kWBytes + (uint32_t)half * kBK;
+        const int wrow = t.group * p.n_out + t.m0 + (int)rank * 128;
+        const int xrow = t.row + (int)rank * half;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait<false>(&st->empty[stage], phase ^ 1u, st, p.err, kErrGemmTimeout | 0x71)) {
+            ok = false;
+            break;
+          }
+          const uint32_t fl = sm100::mapa_shared(sm100::smem_addr(&st->full[stage]), 0);
+          if (leader) sm100::mbar_arrive_expect_tx(&st->full[stage], 2 * bytes);
+          sm100::tma_load_2d_pair(sW(stage, 0), &tw, fl, kb * kBK, wrow);
+          sm100::tma_load_2d_pair(sW(stage, 1), &tw3, fl, kb * kBK, wrow);
+          load_rows(sX(stage), tx, fl, kb * kBK, xrow, half);
+          ++issued;
+          if (++stage == kStagesU) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && leader) settle<kStagesU>(st->full, stage, phase, min(issued, kStagesU));
+    }
+  } else if (warp == 1 || warp == 2) {
+    // issuer `which`: W1 products into columns [0, 256), W3's into [256, 512)
+    if (lane == 0 && leader) {
+      const int which = warp - 1;
+      const uint32_t d_tmem = tmem + (uint32_t)(which * 256);
+      int stage = 0, local = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int tile = pair_id; ok && tile < total; tile += num_pairs, ++local) {
+        const Tile t = decode(tile, p, st->g);
+        if (!wait<true>(&st->tempty, ((uint32_t)local & 1u) ^ 1u, st, p.err,
+                        kErrGemmTimeout | 0x72)) {
+          ok = false;
+          break;
+        }
+        sm100::tc_fence_after();
+        const uint32_t idesc = sm100::idesc_i8_s32(256, t.n);
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!wait<false>(&st->full[stage], phase, st, p.err, kErrGemmTimeout | 0x73)) {
+            ok = false;
+            break;
+          }
+          sm100::tc_fence_after();
+          const uint64_t da = sm100::sw128_kmajor_desc(sm100::smem_addr(sW(stage, which)));
+          const uint64_t db = sm100::sw128_kmajor_desc(sm100::smem_addr(sX(stage)));
+#pragma unroll
+          for (int k = 0; k < kBK / kStep; ++k)
+            sm100::umma_i8_pair(d_tmem, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0);
+          sm100::umma_commit_pair_mc(&st->empty[stage], 0x3);
+          if (++stage == kStagesU) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        sm100::umma_commit_pair_mc(&st->tfull, 0x3);
+      }
+      sm100::umma_commit_pair_mc(&st->drain[which], 0x1);
+      const uint64_t t0 = global_timer_ns();
+      while (!sm100::mbar_try_wait(&st->drain[which], 0) && global_timer_ns() - t0 < kWaitNs) {
+      }
+    }
+  } else if (warp >= 4) {
+    // epilogue: warps q and q + 4 own lanes 32q..32q+31 and take alternate
+    // 32-row groups; u in columns [0, 256), v in [256, 512)
+    const int q = warp & 3;
+    const int half = (warp - 4) >> 2;
+    int local = 0;
+    for (int tile = pair_id; tile < total; tile += num_pairs, ++local) {
+      const Tile t = decode(tile, p, st->g);
+      const int col0 = t.m0 + (int)rank * 128 + 32 * q;
+      const bool real = col0 + lane < p.n_out;  // (a tile may pass the last channel)
+      const size_t wi = (size_t)t.group * p.n_out + col0 + lane;
+      const float ws1 = real ? p.w_scale[wi] : 0.0f, ws3 = real ? p.w3_scale[wi] : 0.0f;
+      if (!wait<true>(&st->tfull, (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x74)) break;
+      sm100::tc_fence_after();
+      const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+#pragma unroll 1
+      for (int cc = 32 * half; cc < t.n; cc += 64) {
+        uint32_t u[32], v[32];
+        sm100::tmem_ld_32x32b_x32(tbase + cc, u);
+        sm100::tmem_ld_32x32b_x32(tbase + 256u + cc, v);
+        emit<OUT>(&staging[warp - 4], p, t, cc, col0, lane, [&](int i, float xs) {
+          return silu_times<OUT>((float)(int)u[i] * (xs * ws1), (float)(int)v[i] * (xs * ws3));
+        });
+      }
+      sm100::tc_fence_before();
+      sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty), 0));
+    }
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::cluster_sync();
+  if (warp == 1) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static std::atomic<EncodeTiledFn> cached{nullptr};
+  EncodeTiledFn f = cached.load();
+  if (f) return f;
+  void* q = nullptr;
+  cudaDriverEntryPointQueryResult r;
+  if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &q, cudaEnableDefault, &r) !=
+          cudaSuccess ||
+      r != cudaDriverEntryPointSuccess)
+    return nullptr;
+  f = reinterpret_cast<EncodeTiledFn>(q);
+  cached.store(f);
+  return f;
+}
+
+// [rows, cols] bytes, boxes of 128 columns, 128-byte swizzle; out of range = 0
+bool byte_map(CUtensorMap* m, const void* ptr, long long rows, long long cols, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t gstride[1] = {(cuuint64_t)cols};
+  const cuuint32_t box[2] = {(cuuint32_t)kBK, (cuuint32_t)box_rows};
+  const cuuint32_t estride[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), gdim, gstride, box,
+            estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <class State>
+constexpr size_t smem_bytes(int ring) {
+  return (size_t)ring + ((sizeof(State) + 127) & ~size_t(127)) + kEpiWarps * sizeof(Staging) + 1024;
+}
+
+template <class K, class... Args>
+cudaError_t launch_i8(K kern, int pairs, size_t bytes, cudaStream_t s, const Args&... args) {
+  const cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), bytes, s, args...);
+}
+
+template <typename OUT>
+cudaError_t run_gemm(const RowMaps& x, const CUtensorMap& w, const CUtensorMap& w3, int act,
+                     const I8Params& p, int pairs, cudaStream_t s) {
+  constexpr size_t stream_bytes = smem_bytes<StreamState>(kStreams * kStagesS * kStageBytesS);
+  constexpr size_t up_bytes = smem_bytes<UpState>(kStagesU * kStageBytesU);
+  static_assert(stream_bytes <= 232448 && up_bytes <= 232448, "227 KB of shared memory");
+  switch (act) {
+    case MOE_I8_SWIGLU:
+      return launch_i8(i8_swiglu_pair_kernel<OUT>, pairs, up_bytes, s, x, w, w3, p);
+    case MOE_I8_RELU:
+      return launch_i8(i8_pair_kernel<OUT, A_RELU>, pairs, stream_bytes, s, x, w, p);
+    case MOE_I8_GELU:
+      return launch_i8(i8_pair_kernel<OUT, A_GELU>, pairs, stream_bytes, s, x, w, p);
+    default:
+      return launch_i8(i8_pair_kernel<OUT, A_NONE>, pairs, stream_bytes, s, x, w, p);
+  }
+}
+
+moe_status i8_check(const moe_gemm_i8_config* c) {
+  if (!c || c->groups < 1 || c->rows < 0 || c->k < 1 || c->n_out < 1) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->act != MOE_I8_NONE && c->act != MOE_I8_RELU && c->act != MOE_I8_GELU &&
+      c->act != MOE_I8_SWIGLU)
+    return MOE_ERR_INVALID_ARG;
+  if (c->groups > MOE_I8_MAX_GROUPS || c->k % 16 || c->k > MOE_I8_MAX_K || c->n_out % 16)
+    return MOE_ERR_UNSUPPORTED;
+  if (c->rows > (1 << 30) || (long long)c->groups * c->n_out > (1LL << 30))
+    return MOE_ERR_UNSUPPORTED;
+  // tile numbers are 32-bit
+  const long long tiles = ((long long)c->rows / kMaxTok + c->groups + 1) * (c->n_out / 256 + 1);
+  if (tiles > (1LL << 30)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_gemm_i8_validate(const moe_gemm_i8_config* cfg) { return i8_check(cfg); }
+
+moe_status moe_gemm_i8_workspace_size(const moe_gemm_i8_config* cfg, size_t* bytes) {
+  moe_status st = i8_check(cfg);
+  if (st != MOE_OK) return st;
+  if (bytes) *bytes = MOE_WS_ERROR_BYTES;
+  return MOE_OK;
+}
+
+moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq, const float* x_scale,
+                       const int32_t* starts, const int32_t* counts, const int8_t* w,
+                       const float* w_scale, const int8_t* w3, const float* w3_scale, void* out,
+                       void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status st = i8_check(cfg);
+  if (st != MOE_OK) return st;
+  if ((starts != nullptr) != (counts != nullptr)) return MOE_ERR_INVALID_ARG;
+  if (!starts && cfg->groups != 1) return MOE_ERR_INVALID_ARG;
+  if (!w || !w_scale) return MOE_ERR_INVALID_ARG;
+  const bool swiglu = cfg->act == MOE_I8_SWIGLU;
+  if (swiglu != (w3 != nullptr) || swiglu != (w3_scale != nullptr)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_block_ws(ws, ws_bytes, MOE_WS_ERROR_BYTES)) != MOE_OK) return st;
+  if (cfg->rows == 0) return MOE_OK;
+  if (!xq || !x_scale || !out) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(xq) || !aligned16(w) || !aligned16(w3) || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  RowMaps x;
+  for (int b = 0; b < kBoxes; ++b)
+    if (!byte_map(&x.m[b], xq, cfg->rows, cfg->k, 16 << b)) return MOE_ERR_CUDA;
+  CUtensorMap mw, mw3;
+  const long long wrows = (long long)cfg->groups * cfg->n_out;
+  if (!byte_map(&mw, w, wrows, cfg->k, 128)) return MOE_ERR_CUDA;
+  mw3 = mw;
+  if (swiglu && !byte_map(&mw3, w3, wrows, cfg->k, 128)) return MOE_ERR_CUDA;
+  I8Params p{};
+  p.starts = starts;
+  p.counts = counts;
+  p.x_scale = x_scale;
+  p.w_scale = w_scale;
+  p.w3_scale = w3_scale;
+  p.groups = cfg->groups;
+  p.rows = cfg->rows;
+  p.K = cfg->k;
+  p.n_out = cfg->n_out;
+  p.mt_tiles = (cfg->n_out + 255) / 256;
+  p.out = out;
+  p.err = static_cast<int*>(ws);
+  // one pair for each two SMs, or one for each tile where there are fewer
+  const long long most = ((long long)cfg->rows / kMaxTok + cfg->groups) * p.mt_tiles;
+  const int pairs = (int)(most < kBlockSms / 2 ? most : kBlockSms / 2);
+  cudaStream_t s = (cudaStream_t)stream;
+  const cudaError_t e = cfg->dtype == MOE_BF16
+                            ? run_gemm<__nv_bfloat16>(x, mw, mw3, cfg->act, p, pairs, s)
+                            : run_gemm<float>(x, mw, mw3, cfg->act, p, pairs, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,383 @@
+// Global norm of many gradient tensors, and their clipping.
+//
+//   norm = (sum_i sum_j g_ij^2)^1/2      c = min(1, max_norm / (norm + 1e-6))
+//   out_i = c g_i
+//
+// Two passes over the data, since c needs every element: the floor is one
+// read and one write, and the second read on top of it is kept small by the
+// order. The tensors are cut into tiles of 8,192 elements, each block takes
+// one contiguous run of tiles, and the scaling pass walks the run backwards,
+// so it begins with what the norm pass read last, which the 126 MB L2 still
+// holds. Both passes are bound by HBM.
+//
+// Squares: eight neighbours are summed in fp32 when the largest of them lies
+// in [2^-50, 2^50] (or all are 0), where neither the squares nor their sum
+// can leave the fp32 range and what underflows is below 2^-40 of the sum;
+// otherwise they are squared in fp64. Everything above eight elements is
+// fp64. Partial sums are per block, in tile order, and each scaling block
+// adds all of them in the same fixed order: no atomics, the same norm in
+// every block and every run.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "block_internal.h"
+#include "device_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTile = 8192;       // elements
+constexpr int kClipThreads = 256;
+constexpr int kClipBlocks = kBlockSms * 6;  // most blocks of a launch (6 resident on an SM)
+constexpr int kUnroll = 4;        // vectors in flight a thread
+
+struct GradTensor {
+  const void* g;
+  void* o;
+  long long n;
+  int tile0;  // tiles of the tensors before it (of this launch)
+  int bf16;
+};
+
+// The tensors of one launch travel in its parameters: 4 KB of them hold what
+// one layer has, the largest parameter block (32,764 bytes) what an unstacked
+// expert list has.
+template <int CAP>
+struct GradBatch {
+  GradTensor t[CAP];
+  int count, tiles;
+};
+constexpr int kSmallBatch = 120, kLargeBatch = 1000;
+static_assert(sizeof(GradBatch<kSmallBatch>) <= 4000, "one 4 KB parameter block");
+static_assert(sizeof(GradBatch<kLargeBatch>) <= 32700, "the largest parameter block");
+
+__device__ __forceinline__ void tile_range(int tiles, int& first, int& last) {
+  first = (int)((long long)blockIdx.x * tiles / gridDim.x);
+  last = (int)((long long)(blockIdx.x + 1) * tiles / gridDim.x);
+}
+
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const GradBatch<CAP>& b, int tile) {
+  int lo = 0, hi = b.count - 1;  // the last tensor with tile0 <= tile (empty ones have no tile)
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (b.t[mid].tile0 <= tile) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <typename T>
+struct Vec16;  // a 16-byte vector of T
+template <>
+struct Vec16<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* v) {
+    v[0] = __uint_as_float(r.x);
+    v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z);
+    v[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                      __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Vec16<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* v) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* v) {
+    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7]));
+  }
+};
+
+template <int N>
+__device__ __forceinline__ double square_sum(const float* v) {
+  float s = 0.0f, m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    s = fmaf(v[i], v[i], s);
+    m = fmaxf(m, fabsf(v[i]));  // (a NaN reaches s)
+  }
+  if (m == 0.0f || (m >= 0x1p-50f && m <= 0x1p50f)) return (double)s;
+  double t = 0.0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) t = fma((double)v[i], (double)v[i], t);
+  return t;
+}
+
+// Elements [0, n) from p on: the vectors between the first and the last
+// 16-byte boundary, and what lies before and behind them one by one.
+template <typename T>
+__device__ __forceinline__ void split16(const T* p, int n, int& head, int& vecs) {
+  constexpr int N = Vec16<T>::N;
+  const int mis = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+  head = min((N - mis) % N, n);
+  vecs = (n - head) / N;
+}
+
+template <typename T>
+__device__ __forceinline__ double tile_squares(const T* p, int n) {
+  constexpr int N = Vec16<T>::N;
+  int head, vecs;
+  split16(p, n, head, vecs);
+  double acc = 0.0;
+  const uint4* q = reinterpret_cast<const uint4*>(p + head);
+  for (int i = threadIdx.x; i < vecs; i += kClipThreads * kUnroll) {
+    uint4 r[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      r[k] = i + k * kClipThreads < vecs ? q[i + k * kClipThreads] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      float v[N];
+      Vec16<T>::unpack(r[k], v);
+      acc += square_sum<N>(v);
+    }
+  }
+  const int tail = head + vecs * N;
+  const int loose = head + n - tail;  // < 2 N
+  if ((int)threadIdx.x < loose) {
+    const int i = (int)threadIdx.x;
+    const float v = (float)p[i < head ? i : tail + i - head];
+    acc += square_sum<1>(&v);
+  }
+  return acc;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* red) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = red[0];
+#pragma unroll
+  for (int i = 1; i < kClipThreads / 32; ++i) s += red[i];
+  return s;
+}
+
+// partial[blockIdx.x] = the sum of squares of the block's tiles
+template <int CAP>
+__global__ void __launch_bounds__(kClipThreads, 6)
+    grad_squares_kernel(const __grid_constant__ GradBatch<CAP> b, double* partial) {
+  __shared__ double red[kClipThreads / 32];
+  pdl_wait();
+  int first, last;
+  tile_range(b.tiles, first, last);
+  int i = find_tensor(b, first);
+  double acc = 0.0;
+  for (int tile = first; tile < last; ++tile) {
+    while (i + 1 < b.count && b.t[i + 1].tile0 <= tile) ++i;
+    const GradTensor& t = b.t[i];
+    const long long at = (long long)(tile - t.tile0) * kTile;
+    const int n = (int)min((long long)kTile, t.n - at);
+    acc += t.bf16 ? tile_squares(static_cast<const __nv_bfloat16*>(t.g) + at, n)
+                  : tile_squares(static_cast<const float*>(t.g) + at, n);
+  }
+  acc = block_sum(acc, red);
+  if (threadIdx.x == 0) partial[blockIdx.x] = acc;
+}
+
+// every block adds the partial sums in the same order
+__device__ __forceinline__ double total_norm(const double* partial, int count, double* red) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < count; i += kClipThreads) s += partial[i];
+  return sqrt(block_sum(s, red));
+}
+
+__global__ void __launch_bounds__(kClipThreads)
+    grad_norm_kernel(const double* partial, int count, float* norm) {
+  __shared__ double red[kClipThreads / 32];
+  pdl_wait();
+  const double r = total_norm(partial, count, red);
+  if (threadIdx.x == 0) norm[0] = (float)r;
+}
+
+template <typename T>
+__device__ __forceinline__ void tile_scale(const T* p, T* o, int n, float c) {
+  constexpr int N = Vec16<T>::N;
+  int head, vecs;
+  split16(p, n, head, vecs);
+  // a copy that is not aligned alike is written element by element
+  if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) {
+    for (int i = threadIdx.x; i < n; i += kClipThreads) o[i] = (T)((float)p[i] * c);
+    return;
+  }
+  const uint4* q = reinterpret_cast<const uint4*>(p + head);
+  uint4* w = reinterpret_cast<uint4*>(o + head);
+  for (int i = threadIdx.x; i < vecs; i += kClipThreads * kUnroll) {
+    uint4 r[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      if (i + k * kClipThreads < vecs) r[k] = __ldcs(q + i + k * kClipThreads);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+      if (i + k * kClipThreads < vecs) {
+        float v[N];
+        Vec16<T>::unpack(r[k], v);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] *= c;
+        __stcs(w + i + k * kClipThreads, Vec16<T>::pack(v));
+      }
+    }
+  }
+  const int tail = head + vecs * N;
+  const int loose = head + n - tail;
+  if ((int)threadIdx.x < loose) {
+    const int j = (int)threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
+    o[j] = (T)((float)p[j] * c);
+  }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kClipThreads, 6)
+    grad_scale_kernel(const __grid_constant__ GradBatch<CAP> b, const double* partial, int count,
+                      float max_norm, float* norm, int write_norm) {
+  __shared__ double red[kClipThreads / 32];
+  pdl_wait();
+  const double r = total_norm(partial, count, red);
+  const double k = (double)max_norm / (r + 1e-6);
+  const float c = isnan(r) ? (float)r : (float)(k < 1.0 ? k : 1.0);
+  if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) {
+    norm[0] = (float)r;
+    norm[1] = c;
+  }
+  if (b.tiles == 0) return;
+  int first, last;
+  tile_range(b.tiles, first, last);
+  int i = find_tensor(b, last - 1);
+  for (int tile = last - 1; tile >= first; --tile) {
+    // (tensors without elements share their successor's tile0)
+    while (b.t[i].tile0 > tile) --i;
+    const GradTensor& t = b.t[i];
+    if (c == 1.0f && t.g == t.o) continue;
+    const long long at = (long long)(tile - t.tile0) * kTile;
+    const int n = (int)min((long long)kTile, t.n - at);
+    if (t.bf16)
+      tile_scale(static_cast<const __nv_bfloat16*>(t.g) + at, static_cast<__nv_bfloat16*>(t.o) + at,
+                 n, c);
+    else
+      tile_scale(static_cast<const float*>(t.g) + at, static_cast<float*>(t.o) + at, n, c);
+  }
+}
+
+int batches(int count) { return count <= kSmallBatch ? 1 : (count + kLargeBatch - 1) / kLargeBatch; }
+
+size_t clip_bytes(int count) { return (size_t)batches(count) * kClipBlocks * sizeof(double); }
+
+moe_status check_tensors(const moe_grad_tensor* t, int count, bool outs) {
+  if (count < 0 || (count > 0 && !t)) return MOE_ERR_INVALID_ARG;
+  long long tiles = 0;
+  for (int i = 0; i < count; ++i) {
+    if (t[i].numel < 0 || (t[i].dtype != MOE_F32 && t[i].dtype != MOE_BF16))
+      return MOE_ERR_INVALID_ARG;
+    if (t[i].numel == 0) continue;
+    const uintptr_t mask = t[i].dtype == MOE_BF16 ? 1 : 3;
+    if (!t[i].grad || (reinterpret_cast<uintptr_t>(t[i].grad) & mask)) return MOE_ERR_INVALID_ARG;
+    if (outs && (!t[i].out || (reinterpret_cast<uintptr_t>(t[i].out) & mask)))
+      return MOE_ERR_INVALID_ARG;
+    if (t[i].numel > (1LL << 42)) return MOE_ERR_UNSUPPORTED;
+    tiles += (t[i].numel + kTile - 1) / kTile;
+    if (tiles > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
+  }
+  return MOE_OK;
+}
+
+// the tensors with elements of [first, first + CAP)
+template <int CAP>
+void fill(GradBatch<CAP>& b, const moe_grad_tensor* t, int first, int count) {
+  b.count = 0;
+  b.tiles = 0;
+  for (int i = first; i < count && i < first + CAP; ++i) {
+    if (t[i].numel == 0) continue;
+    GradTensor& g = b.t[b.count++];
+    g.g = t[i].grad;
+    g.o = t[i].out;
+    g.n = t[i].numel;
+    g.tile0 = b.tiles;
+    g.bf16 = t[i].dtype == MOE_BF16;
+    b.tiles += (int)((t[i].numel + kTile - 1) / kTile);
+  }
+}
+
+int clip_grid(int tiles) { return tiles < kClipBlocks ? tiles : kClipBlocks; }
+
+template <int CAP>
+moe_status run_clip(const moe_grad_tensor* t, int count, bool scale, float max_norm, float* norm,
+                    double* partial, cudaStream_t s) {
+  GradBatch<CAP> b;  // (32 KB at most, on the host's stack)
+  int used = 0;
+  for (int first = 0; first < count; first += CAP) {
+    fill(b, t, first, count);
+    if (b.tiles == 0) continue;
+    const int grid = clip_grid(b.tiles);
+    if (launch_pdl(grad_squares_kernel<CAP>, dim3(grid), dim3(kClipThreads), 0, s, b,
+                   partial + used) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    used += grid;
+  }
+  if (!scale) {
+    return launch_pdl(grad_norm_kernel, dim3(1), dim3(kClipThreads), 0, s,
+                      (const double*)partial, used, norm) == cudaSuccess
+               ? MOE_OK
+               : MOE_ERR_CUDA;
+  }
+  // the last tensors first: L2 holds them
+  int write = 1;
+  for (int first = count > 0 ? (count - 1) / CAP * CAP : 0; first >= 0; first -= CAP) {
+    fill(b, t, first, count);
+    if (b.tiles == 0 && !(write && first == 0)) continue;
+    const int grid = b.tiles ? clip_grid(b.tiles) : 1;
+    if (launch_pdl(grad_scale_kernel<CAP>, dim3(grid), dim3(kClipThreads), 0, s, b,
+                   (const double*)partial, used, max_norm, norm, write) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    write = 0;
+  }
+  return MOE_OK;
+}
+
+moe_status clip_impl(const moe_grad_tensor* t, int count, bool scale, float max_norm, float* norm,
+                     void* ws, size_t ws_bytes, cudaStream_t s) {
+  moe_status st = check_tensors(t, count, scale);
+  if (st != MOE_OK) return st;
+  if (!norm || (reinterpret_cast<uintptr_t>(norm) & 3)) return MOE_ERR_INVALID_ARG;
+  if ((st = check_block_ws(ws, ws_bytes, clip_bytes(count))) != MOE_OK) return st;
+  double* partial = static_cast<double*>(ws);
+  return count <= kSmallBatch
+             ? run_clip<kSmallBatch>(t, count, scale, max_norm, norm, partial, s)
+             : run_clip<kLargeBatch>(t, count, scale, max_norm, norm, partial, s);
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_grad_workspace_size(int count, size_t* bytes) {
+  if (count < 0) return MOE_ERR_INVALID_ARG;
+  if (bytes) *bytes = clip_bytes(count);
+  return MOE_OK;
+}
+
+moe_status moe_grad_norm(const moe_grad_tensor* tensors, int count, float* norm, void* ws,
+                         size_t ws_bytes, moe_stream_t stream) {
+  return clip_impl(tensors, count, false, 0.0f, norm, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+moe_status moe_grad_clip(const moe_grad_tensor* tensors, int count, float max_norm, float* norm,
+                         void* ws, size_t ws_bytes, moe_stream_t stream) {
+  if (!(max_norm >= 0.0f)) return MOE_ERR_INVALID_ARG;
+  return clip_impl(tensors, count, true, max_norm, norm, ws, ws_bytes, (cudaStream_t)stream);
+}
+
+}  // extern "C"

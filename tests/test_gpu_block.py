@@ -1,0 +1,162 @@
+"""A block (pre-norm, layer, post-norm with gate and residual, next pre-norm)
+run as a user runs it: serving, training with the clip, and in a graph."""
+import math
+
+import pytest
+import torch
+
+import block_ref as R
+from expert_dispatch_gemm_b200 import block, moe
+from expert_dispatch_gemm_b200 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+def near(got, want, rel_mag, rounding, name):
+    tol = rounding * want.abs() + rel_mag + 1e-37
+    off = (got.double() - want).abs() - tol
+    assert bool((off <= 0).all()), (name, off.max().item())
+
+
+def make(w, seed=3, tokens=100, gate=True):
+    inp = wl.make_inputs(w, DEV)
+    g = gen(seed)
+    f = lambda: 1 + 0.1 * torch.randn(w.d, generator=g, device=DEV)  # noqa: E731
+    p = {"w_pre": f(), "w_post": f(), "w_next": f()}
+    if gate:
+        p["gate"] = (0.5 * torch.randn((-(-w.n // tokens) if tokens else 1, w.d), generator=g,
+                                       device=DEV)).to(w.torch_dtype)
+    b = block.Block(moe.Layer(w, inp, DEV), p, eps=1e-5, gate_tokens=tokens, block_scale=0.5)
+    x = torch.randn((w.n, w.d), generator=g, device=DEV).to(w.torch_dtype)
+    dout = torch.randn((w.n, w.d), generator=g, device=DEV).to(w.torch_dtype)
+    dh = torch.randn((w.n, w.d), generator=g, device=DEV).to(w.torch_dtype)
+    return b, p, x, dout, dh
+
+
+@pytest.mark.parametrize("w", [wl.EC_FP32, wl.SMALL[2], wl.SMALL[3], wl.SMALL[4]],
+                         ids=lambda w: w.name)
+def test_train_step(w):
+    b, p, x, dout, dh = make(w)
+    out, h_next = b.forward_train(x)
+    g = b.backward_train(dout, dh)
+    torch.cuda.synchronize()
+    step = R.half_step(w.torch_dtype)
+    kw = dict(b=0.5, tokens=100)
+    # forward: each step from what the one before it stored
+    h, r = R.norm(x.double(), p["w_pre"], 0.0, 1e-5)
+    near(b.h, h, 2 * R.ROW * h.abs(), step, "h")
+    y = b.layer.out
+    ref, hn, r1, r2 = R.residual_norm(x.double(), y.double(), p["w_post"], p["gate"],
+                                      p["w_next"], eps=1e-5, **kw)
+    terms = x.double().abs() + (ref - x.double()).abs()
+    near(out, ref, R.ROW * terms, step, "out")
+    scale = r2[:, None] * p["w_next"].double().abs()
+    mix = 1 + (terms * ref.abs()).mean(1, keepdim=True) / (ref * ref).mean(1, keepdim=True)
+    near(h_next, hn, R.ROW * (terms * scale + mix * hn.abs()), step, "h_next")
+    # backward
+    rows = b.p["gate"].shape[0]
+    args = [t.double() for t in (dout, dh, out, y)] + [p["w_post"], p["gate"], p["w_next"],
+                                                       b.r_post.double(), b.r_next.double()]
+    want = R.residual_norm_backward(*args, gate_rows=rows, **kw)
+    mag = R.residual_norm_backward(*args, gate_rows=rows, magnitudes=True, **kw)
+    chain = R.ROW + (w.n + 4000) * R.U
+    near(g["dy"], want[1], 3 * R.ROW * mag[1], step, "dy")
+    near(g["dw_post"], want[2], (2 * R.ROW + chain) * mag[2], R.U, "dw_post")
+    near(g["dgate"], want[3], (2 * R.ROW + chain) * mag[3], step, "dgate")
+    near(g["dw_next"], want[4], chain * mag[4], R.U, "dw_next")
+    # the layer's own gradient is what moe.Layer gives for dy
+    lg = {k: None if t is None else t.clone() for k, t in g["layer"].items()}
+    layer2 = moe.Layer(w, b.layer.inp, DEV)
+    layer2.forward_train(X=b.h)
+    again = layer2.backward_train(g["dy"], X=b.h)
+    for k in ("dX", "dW1", "dWg"):
+        assert torch.equal(lg[k], again[k]), k
+    # dx: the residual's share was rounded once before the pre-norm's was added
+    args = (want[0], lg["dX"].double(), x.double(), torch.zeros_like(h), None, None, p["w_pre"],
+            None, b.r_pre.double())
+    dx = R.residual_norm_backward(*args)
+    dmag = R.residual_norm_backward(*args, magnitudes=True)
+    near(g["dx"], dx[0], step * want[0].abs() + 4 * R.ROW * (dmag[0] + mag[0]), step, "dx")
+    near(g["dw_pre"], dx[4], chain * dmag[4] + 2 * R.ROW * dmag[4], R.U, "dw_pre")
+    # clip: every parameter's gradient, in place
+    names = ["dw_pre", "dw_post", "dgate", "dw_next"]
+    params = [g[k] for k in names] + [t for k, t in g["layer"].items()
+                                      if t is not None and k not in ("dX", "dL")]
+    before = [t.clone() for t in params]
+    total = math.sqrt(sum(float((t.double() ** 2).sum()) for t in before))
+    norm, factor = b.clip_grads(0.25 * total).tolist()
+    assert abs(norm - total) <= 10 * R.U * total
+    for t, o in zip(params, before):
+        near(t, o.double() * (0.25 * total / (total + 1e-6)), 14 * R.U * o.double().abs(), step,
+             "clipped")
+    assert abs(factor - 0.25) < 1e-6
+    # one more clip finds the norm inside the limit (or a rounding above it)
+    norm2, factor2 = b.clip_grads(0.2501 * total).tolist()
+    assert norm2 <= 0.2501 * total and factor2 == 1.0
+
+
+def test_block_without_optional_parts():
+    w = wl.SMALL[3]
+    inp = wl.make_inputs(w, DEV)
+    p = {"w_pre": torch.ones(w.d, device=DEV)}
+    b = block.Block(moe.Layer(w, inp, DEV), p)
+    x = inp["X"]
+    out, h_next = b.forward_train(x)
+    assert h_next is None
+    want = x.double() + b.layer.out.double()
+    near(out, want, 2 * R.U * (x.double().abs() + b.layer.out.double().abs()),
+         R.half_step(out.dtype), "out")
+    dout = torch.randn_like(out)
+    g = b.backward_train(dout)
+    assert torch.equal(g["dy"], dout)
+    assert b.clip_grads(1.0)[1].item() < 1.0
+
+
+def test_serving_with_8_bit_experts():
+    w = wl.SMALL[4]
+    inp = wl.make_inputs(w, DEV)
+    p = {"w_pre": torch.ones(w.d, device=DEV), "w_post": torch.ones(w.d, device=DEV),
+         "w_next": torch.ones(w.d, device=DEV)}
+    exact = block.Block(moe.Layer(w, inp, DEV), p)
+    fast = block.Block(block.QuantizedLayer(w, inp, DEV), p)
+    x = inp["X"]
+    a, ha = exact.forward(x)
+    b, hb = fast.forward(x)
+    for s, t in ((a, b), (ha, hb)):
+        # the layer's 6% (see the quantised layer's test) before a residual of equal size
+        assert (s.double() - t.double()).norm() / s.double().norm() < 0.06
+
+
+def test_decode_step_in_a_graph():
+    """Two blocks in a row on one token batch, the first one's fused next
+    pre-norm feeding a layer, captured and replayed on new tokens."""
+    w = wl.SMALL[4].replace(name="decode", n=5)
+    inp = wl.make_inputs(w, DEV)
+    p = {k: torch.ones(w.d, device=DEV) for k in ("w_pre", "w_post", "w_next")}
+    one = block.Block(block.QuantizedLayer(w, inp, DEV), p)
+    two = block.QuantizedLayer(w, inp, DEV)
+    x = inp["X"].clone()
+
+    def step():
+        _, h = one.forward(x)
+        return two.forward(h)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in (1, 2):
+        x.copy_(torch.randn(x.shape, generator=gen(seed), device=DEV))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = two.out.clone(), one.out.clone()
+        want = step().clone(), one.out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    del graph
