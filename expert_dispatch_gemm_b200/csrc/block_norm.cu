@@ -18,8 +18,15 @@
 //   m = (sum (dout + r2 q) c - r2 mean(q u) sum u c) / d,
 // so a row takes one block reduction (of three sums), not two in sequence.
 //
-// All four kernels are bound by HBM: the forward moves 4 n d elements (x, y,
-// out, h), the backward 6 n d.
+// The forward moves 4 n d elements (x, y, out, h), the backward 6 n d: both are
+// to be bound by HBM, which leaves about 20 instructions an element. So
+// - a block (worker) owns a contiguous range of rows, and a thread the same 8
+//   columns (16 above d = 8192) of each: weights, the gate's product with them
+//   and the sums over tokens stay in its registers;
+// - arithmetic is on packed fp32 pairs;
+// - the next rows' chunks come into shared memory by cp.async while a row is
+//   computed; each thread reads back only what it copied itself, so no barrier
+//   guards the ring, and the only barriers are those of the row sums.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,88 +38,107 @@
 namespace moe {
 namespace {
 
-// ---- VEC consecutive elements of a row ------------------------------------
-template <typename T, int VEC>
-struct Chunk;
-template <>
-struct Chunk<__nv_bfloat16, 8> {
-  uint4 r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = __ldcs(reinterpret_cast<const uint4*>(p));
-  }
-  __device__ __forceinline__ void load_smem(const void* p) {
-    r = *reinterpret_cast<const uint4*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ float get(int i) const {
-    const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
-    return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
-  }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                              pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  }
-};
-template <>
-struct Chunk<float, 4> {
-  float4 r;
-  __device__ __forceinline__ void load(const float* p) {
-    r = __ldcs(reinterpret_cast<const float4*>(p));
-  }
-  __device__ __forceinline__ void load_smem(const void* p) {
-    r = *reinterpret_cast<const float4*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = make_float4(0, 0, 0, 0); }
-  __device__ __forceinline__ float get(int i) const {
-    return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float* v) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  }
-};
-template <>
-struct Chunk<__nv_bfloat16, 1> {
-  uint16_t r;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    r = *reinterpret_cast<const uint16_t*>(p);
-  }
-  __device__ __forceinline__ void load_smem(const void* p) {
-    r = *reinterpret_cast<const uint16_t*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = 0; }
-  __device__ __forceinline__ float get(int) const { return bf16_to_f32(r); }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* v) {
-    *p = __float2bfloat16_rn(v[0]);
-  }
-};
-template <>
-struct Chunk<float, 1> {
-  float r;
-  __device__ __forceinline__ void load(const float* p) { r = *p; }
-  __device__ __forceinline__ void load_smem(const void* p) {
-    r = *reinterpret_cast<const float*>(p);
-  }
-  __device__ __forceinline__ void zero() { r = 0.0f; }
-  __device__ __forceinline__ float get(int) const { return r; }
-  static __device__ __forceinline__ void store(float* p, const float* v) { *p = v[0]; }
-};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// VEC fp32 weights (read by every row: they stay in L1)
-template <int VEC>
-__device__ __forceinline__ void load_weights(float* w, const float* p, float off) {
-  if constexpr (VEC == 1) {
-    w[0] = __ldg(p) + off;
-  } else {
+// A thread's EPT elements of a row, as pairs: EPT / VEC chunks of VEC
+// neighbours, chunk c of the row at thread c % threads, so that an access of
+// the warp is one run of 16-byte vectors (VEC = 1: of single elements, for
+// rows that do not start on 16-byte boundaries). Columns past d are zeros.
+template <typename T, int VEC, int EPT>
+struct Cols {
+  static constexpr int ITEMS = EPT / VEC;
+  int tid, threads, chunks;
+
+  __device__ __forceinline__ bool has(int i) const { return i * threads + tid < chunks; }
+  __device__ __forceinline__ int at(int i) const { return (i * threads + tid) * VEC; }
+
+  // SMEM: a row that this thread copied itself; else global
+  template <bool SMEM>
+  __device__ __forceinline__ void load(float2* v, const T* row) const {
+    if constexpr (VEC == 1) {
 #pragma unroll
-    for (int i = 0; i < VEC; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p + i));
-      w[i] = v.x + off;
-      w[i + 1] = v.y + off;
-      w[i + 2] = v.z + off;
-      w[i + 3] = v.w + off;
+      for (int i = 0; i < EPT; ++i) {
+        const float x = has(i) ? (float)row[at(i)] : 0.0f;
+        if (i & 1) v[i / 2].y = x; else v[i / 2].x = x;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (has(i)) {
+          const uint4* q = reinterpret_cast<const uint4*>(row + at(i));
+          r = SMEM ? *q : __ldcs(q);
+        }
+        float2* o = v + i * (VEC / 2);
+        if constexpr (sizeof(T) == 4) {
+          o[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+          o[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+        } else {
+          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            o[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+        }
+      }
     }
   }
-}
+  __device__ __forceinline__ void store(T* row, const float2* v) const {
+    if constexpr (VEC == 1) {
+#pragma unroll
+      for (int i = 0; i < EPT; ++i)
+        if (has(i)) row[at(i)] = (T)((i & 1) ? v[i / 2].y : v[i / 2].x);
+    } else {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        if (!has(i)) continue;
+        const float2* o = v + i * (VEC / 2);
+        if constexpr (sizeof(T) == 4)
+          *reinterpret_cast<float4*>(row + at(i)) = make_float4(o[0].x, o[0].y, o[1].x, o[1].y);
+        else
+          *reinterpret_cast<uint4*>(row + at(i)) =
+              make_uint4(pack_bf16x2(o[0].x, o[0].y), pack_bf16x2(o[1].x, o[1].y),
+                         pack_bf16x2(o[2].x, o[2].y), pack_bf16x2(o[3].x, o[3].y));
+      }
+    }
+  }
+  // fp32 rows of the same columns (weights, sums), element by element aligned
+  // as the vectors need it
+  __device__ __forceinline__ void load_f32(float2* v, const float* row) const {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if constexpr (VEC == 1) {
+        const float x = has(i) ? row[at(i)] : 0.0f;
+        if (i & 1) v[i / 2].y = x; else v[i / 2].x = x;
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+          float4 w = make_float4(0, 0, 0, 0);
+          if (has(i)) w = *reinterpret_cast<const float4*>(row + at(i) + j);
+          v[(i * VEC + j) / 2] = make_float2(w.x, w.y);
+          v[(i * VEC + j) / 2 + 1] = make_float2(w.z, w.w);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store_f32(float* row, const float2* v) const {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      if (!has(i)) continue;
+      if constexpr (VEC == 1) {
+        row[at(i)] = (i & 1) ? v[i / 2].y : v[i / 2].x;
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j += 4) {
+          const float2 a = v[(i * VEC + j) / 2], b = v[(i * VEC + j) / 2 + 1];
+          *reinterpret_cast<float4*>(row + at(i) + j) = make_float4(a.x, a.y, b.x, b.y);
+        }
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -120,16 +146,34 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sum over the threads of a row: the warp, or (block rows) all of the block's
-// warps through `red` [32], which the caller does not reuse before another
-// block barrier.
-__device__ __forceinline__ float row_sum(float v, float* red, bool block_row) {
-  v = warp_sum(v);
-  if (!block_row) return v;
-  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (lane == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  return warp_sum(lane < warps ? red[lane] : 0.0f);
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// the oldest row of a ring of `stages` has arrived
+__device__ __forceinline__ void cp_async_wait_row(int stages) {
+  if (stages >= 4) cp_async_wait<3>();
+  else if (stages == 3) cp_async_wait<2>();
+  else if (stages == 2) cp_async_wait<1>();
+  else cp_async_wait<0>();
+}
+constexpr int kMaxStages = 4;
+
+__host__ __device__ __forceinline__ int worker_row(int w, int n, int workers) {
+  return (int)((long long)w * n / workers);
+}
+// the worker that holds row r
+__host__ __device__ __forceinline__ int row_worker(int r, int n, int workers) {
+  return (int)((((long long)r + 1) * workers - 1) / n);
 }
 
 // ---------------------------------------------------------------------------
@@ -140,124 +184,169 @@ struct NormFwd {
   const float *w_post, *w_next;
   void *out, *h;
   float *rstd_post, *rstd_next;
-  int n, d, gate_tokens;
+  int n, d, gate_tokens, workers, stages, slots;
   float eps, off, a, b;
   long long gate_stride;
 };
 
-// A row belongs to one warp (blockDim = 32 x rows: narrow rows) or to the
-// whole block (blockDim = threads x 1). Each thread keeps ITEMS chunks of
-// x and y in registers from the one read to the writes, chunk c of the row at
-// thread c % threads, so that every access is one coalesced 16-byte vector.
-template <typename T, int VEC, int ITEMS, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_fwd_kernel(const NormFwd p) {
-  __shared__ float red[2][32];
+// The sum of v over the block: within the warps, then over their sums in
+// `red`, which nothing else may use until the block's next barrier but one.
+__device__ __forceinline__ float block_sum(float v, float* red, int warps) {
+  v = warp_sum(v);
+  if (warps == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  // (every lane of a group of 8, 16 or 32 holds one warp's sum)
+  const int group = warps <= 8 ? 8 : warps <= 16 ? 16 : 32;
+  const int i = lane & (group - 1);
+  v = i < warps ? red[i] : 0.0f;
+  for (int o = group / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int VEC, int EPT, bool STAGED>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p) {
+  extern __shared__ __align__(16) unsigned char nsm[];
+  __shared__ float red[2][2][32];
   pdl_wait();
-  const int row = blockIdx.x * blockDim.y + threadIdx.y;
-  if (row >= p.n) return;  // (warp rows only: no barrier follows)
-  const bool block_row = blockDim.x > 32;
-  const int tid = threadIdx.x, threads = blockDim.x;
-  const int chunks = p.d / VEC;
-  const size_t base = (size_t)row * p.d;
-  const T* x = static_cast<const T*>(p.x) + base;
-  const T* y = p.y ? static_cast<const T*>(p.y) + base : nullptr;
-  using C = Chunk<T, VEC>;
-  C cx[ITEMS], cy[ITEMS];
+  constexpr int P = EPT / 2;
+  const Cols<T, VEC, EPT> cols{(int)threadIdx.x, (int)blockDim.x, p.d / VEC};
+  const int warps = blockDim.x >> 5;
+  const int w = blockIdx.x;
+  const int r0 = worker_row(w, p.n, p.workers), r1 = worker_row(w + 1, p.n, p.workers);
+  const T* gx = static_cast<const T*>(p.x);
+  const T* gy = static_cast<const T*>(p.y);
+  const T* gate = static_cast<const T*>(p.gate);
+  const bool gate_each = gate && p.gate_tokens == 1;  // its rows travel with the others
+  const size_t row_bytes = (size_t)p.d * sizeof(T);
+  const float inv_d = 1.0f / (float)p.d;
+  auto issue = [&](int r) {
+    if constexpr (STAGED) {
+      if (r < r1) {
+        unsigned char* st = nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes;
+        const size_t base = (size_t)r * p.d;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int c = i * threads + tid;
-    cx[i].zero();
-    cy[i].zero();
-    if (c < chunks) {
-      if (y) cy[i].load(y + c * VEC);
-      cx[i].load(x + c * VEC);
-    }
-  }
-  float o[ITEMS * VEC];
-  float ss = 0.0f;
-  if (y) {
-    float r1 = 1.0f;
-    if (p.w_post) {
-      float s = 0.0f;
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) s = fmaf(cy[i].get(j), cy[i].get(j), s);
-      s = row_sum(s, red[0], block_row);
-      r1 = rsqrtf(s / (float)p.d + p.eps);
-      if (p.rstd_post && tid == 0) p.rstd_post[row] = r1;
-    }
-    const T* gate = nullptr;
-    if (p.gate)
-      gate = static_cast<const T*>(p.gate) +
-             (p.gate_tokens ? (long long)(row / p.gate_tokens) * p.gate_stride : 0);
-    T* out = static_cast<T*>(p.out) + base;
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int c = i * threads + tid;
-      if (c < chunks) {
-        float w[VEC];
-        C g;
-        if (p.w_post) load_weights<VEC>(w, p.w_post + c * VEC, p.off);
-        if (gate) g.load(gate + c * VEC);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          float v = cy[i].get(j);
-          if (p.w_post) v = v * r1 * w[j];
-          if (gate) v *= g.get(j);
-          o[i * VEC + j] = fmaf(p.a, cx[i].get(j), p.b * v);
+        for (int i = 0; i < cols.ITEMS; ++i) {
+          if (!cols.has(i)) continue;
+          unsigned char* dst = st + (size_t)cols.at(i) * sizeof(T);
+          cp_async16(dst, gx + base + cols.at(i));
+          if (gy) cp_async16(dst + row_bytes, gy + base + cols.at(i));
+          if (gate_each)
+            cp_async16(dst + 2 * row_bytes, gate + (long long)r * p.gate_stride + cols.at(i));
         }
-        C::store(out + c * VEC, o + i * VEC);
+      }
+      cp_async_commit();
+    }
+  };
+  for (int q = 0; q < p.stages - 1; ++q) issue(r0 + q);
+  float2 cw[P], wn[P];  // b gate (w_post + off); w_next + off
+  if (p.h) {
+    cols.load_f32(wn, p.w_next);
+#pragma unroll
+    for (int e = 0; e < P; ++e) wn[e] = add2(wn[e], both(p.off));
+  }
+  for (int r = r0; r < r1; ++r) {
+    issue(r + p.stages - 1);
+    if (STAGED) cp_async_wait_row(p.stages);
+    const size_t base = (size_t)r * p.d;
+    const T* st = reinterpret_cast<const T*>(
+        nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes);
+    if (gy && (r == r0 || (gate && p.gate_tokens && r % p.gate_tokens == 0))) {
+      if (p.w_post) {
+        cols.load_f32(cw, p.w_post);
+#pragma unroll
+        for (int e = 0; e < P; ++e) cw[e] = mul2(add2(cw[e], both(p.off)), both(p.b));
       } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) o[i * VEC + j] = 0.0f;
+        for (int e = 0; e < P; ++e) cw[e] = both(p.b);
+      }
+      if (gate) {
+        float2 g[P];
+        if (STAGED && gate_each)
+          cols.template load<true>(g, st + 2 * p.d);
+        else
+          cols.template load<false>(
+              g, gate + (p.gate_tokens ? (long long)(r / p.gate_tokens) * p.gate_stride : 0));
+#pragma unroll
+        for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], g[e]);
       }
     }
-  } else {
+    float2 o[P];
+    if (gy) {
+      float2 y[P];
+      cols.template load<STAGED>(y, STAGED ? st + p.d : gy + base);
+      if (!STAGED) cols.template load<false>(o, gx + base);
+      float rp = 1.0f;
+      if (p.w_post) {
+        float2 s = both(0.0f);
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
+        for (int e = 0; e < P; ++e) s = fma2(y[e], y[e], s);
+        const float ss = block_sum(s.x + s.y, red[r & 1][0], warps);
+        rp = rsqrtf(ss * inv_d + p.eps);
+        if (p.rstd_post && threadIdx.x == 0) p.rstd_post[r] = rp;
+      }
+      if (STAGED) cols.template load<true>(o, st);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) o[i * VEC + j] = cx[i].get(j);
-  }
-  if (!p.h) return;
+      for (int e = 0; e < P; ++e)
+        o[e] = fma2(mul2(y[e], cw[e]), both(rp), mul2(o[e], both(p.a)));
+      cols.store(static_cast<T*>(p.out) + base, o);
+    } else {
+      cols.template load<STAGED>(o, STAGED ? st : gx + base);
+    }
+    if (p.h) {
+      float2 s = both(0.0f);
 #pragma unroll
-  for (int i = 0; i < ITEMS * VEC; ++i) ss = fmaf(o[i], o[i], ss);
-  ss = row_sum(ss, red[1], block_row);
-  const float r2 = rsqrtf(ss / (float)p.d + p.eps);
-  if (p.rstd_next && tid == 0) p.rstd_next[row] = r2;
-  T* h = static_cast<T*>(p.h) + base;
+      for (int e = 0; e < P; ++e) s = fma2(o[e], o[e], s);
+      const float ss = block_sum(s.x + s.y, red[r & 1][1], warps);
+      const float rn = rsqrtf(ss * inv_d + p.eps);
+      if (p.rstd_next && threadIdx.x == 0) p.rstd_next[r] = rn;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int c = i * threads + tid;
-    if (c < chunks) {
-      float w[VEC];
-      load_weights<VEC>(w, p.w_next + c * VEC, p.off);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) o[i * VEC + j] = o[i * VEC + j] * r2 * w[j];
-      C::store(h + c * VEC, o + i * VEC);
+      for (int e = 0; e < P; ++e) o[e] = mul2(mul2(o[e], both(rn)), wn[e]);
+      cols.store(static_cast<T*>(p.h) + base, o);
     }
   }
 }
 
-template <typename T, int VEC, int ITEMS, int MAXT>
-cudaError_t run_fwd(const NormFwd& p, dim3 grid, dim3 block, cudaStream_t s) {
-  return launch_pdl(norm_fwd_kernel<T, VEC, ITEMS, MAXT>, grid, block, 0, s, p);
+// ---- work split --------------------------------------------------------------
+// Threads a worker: 8 columns each up to d = 8192, 16 above.
+int norm_threads(int d) { return ((d <= 8192 ? (d + 7) / 8 : (d + 15) / 16) + 31) / 32 * 32; }
+// shared memory for one worker's ring where `per_sm` of them share an SM
+size_t ring_budget(int per_sm) { return (size_t)(224 * 1024) / per_sm - 2048; }
+
+int fwd_workers_per_sm(int d) {
+  const int k = 1024 / norm_threads(d);
+  return k < 1 ? 1 : k > 16 ? 16 : k;
 }
 
-// Narrow rows (up to 32 elements a lane with vectors, 8 without): a warp
-// each, four to a block. Wider ones: a block each, with 16 elements a thread
-// (32 where 1024 threads would not reach).
+template <typename T, int VEC, int EPT, bool STAGED>
+cudaError_t run_fwd(const NormFwd& p, size_t smem, cudaStream_t s) {
+  auto kern = norm_fwd_kernel<T, VEC, EPT, STAGED>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(p.workers), dim3(norm_threads(p.d)), smem, s, p);
+}
+
 template <typename T, int VEC>
-cudaError_t launch_fwd(const NormFwd& p, cudaStream_t s) {
-  constexpr int E16 = VEC == 1 ? 16 : 16 / VEC;  // chunks a thread for 16 elements
-  constexpr int E8 = VEC == 1 ? 8 : 8 / VEC;
-  const int chunks = p.d / VEC;
-  constexpr int kRows = 4;
-  const dim3 wgrid((p.n + kRows - 1) / kRows), wblock(32, kRows);
-  if (chunks <= 32 * E8) return run_fwd<T, VEC, E8, 128>(p, wgrid, wblock, s);
-  if (VEC > 1 && chunks <= 32 * E16) return run_fwd<T, VEC, E16, 128>(p, wgrid, wblock, s);
-  const int threads = ((chunks + E16 - 1) / E16 + 31) / 32 * 32;
-  return run_fwd<T, VEC, E16, 1024>(p, dim3(p.n), dim3(threads), s);
+cudaError_t launch_fwd(NormFwd& p, bool vec, cudaStream_t s) {
+  const int per_sm = fwd_workers_per_sm(p.d);
+  const long long most = (long long)kBlockSms * per_sm;
+  p.workers = (int)(p.n < most ? p.n : most);
+  p.slots = p.gate && p.gate_tokens == 1 ? 3 : p.y ? 2 : 1;
+  const size_t row = (size_t)p.d * sizeof(T);
+  const size_t fit = ring_budget(per_sm) / (p.slots * row);
+  const int deep = (p.n + p.workers - 1) / p.workers;  // no more stages than rows
+  p.stages = fit > kMaxStages ? kMaxStages : (int)fit;
+  if (p.stages > deep) p.stages = deep;
+  if (!vec || p.stages < 1) {
+    p.stages = 1;
+    return p.d > 8192 ? run_fwd<T, 1, 16, false>(p, 0, s) : run_fwd<T, 1, 8, false>(p, 0, s);
+  }
+  const size_t smem = p.stages * p.slots * row;
+  return p.d > 8192 ? run_fwd<T, VEC, 16, true>(p, smem, s) : run_fwd<T, VEC, 8, true>(p, smem, s);
 }
 
 // ---------------------------------------------------------------------------
@@ -278,242 +367,238 @@ struct NormBwd {
   long long gate_stride;
 };
 
-__host__ __device__ __forceinline__ int worker_row(int w, int n, int workers) {
-  return (int)((long long)w * n / workers);
+// Three sums over the block at once. Within a warp, halves of the lanes first
+// trade values so that each lane carries one sum (18 instructions instead of
+// 30); the warps' sums then meet in `red` as one 16-byte vector a warp.
+__device__ __forceinline__ float sum3_lanes(float a, float b, float c, int lane) {
+  const bool h16 = lane & 16, h8 = lane & 8;
+  float k0 = h16 ? c : a, k1 = h16 ? 0.0f : b;
+  k0 += __shfl_xor_sync(0xffffffffu, h16 ? a : c, 16);
+  k1 += __shfl_xor_sync(0xffffffffu, h16 ? b : 0.0f, 16);
+  float k = h8 ? k1 : k0;
+  k += __shfl_xor_sync(0xffffffffu, h8 ? k0 : k1, 8);
+  k += __shfl_xor_sync(0xffffffffu, k, 4);
+  k += __shfl_xor_sync(0xffffffffu, k, 2);
+  k += __shfl_xor_sync(0xffffffffu, k, 1);
+  return k;  // lanes 0-7: a, 8-15: b, 16-23: c
 }
-// the worker that holds row r
-__host__ __device__ __forceinline__ int row_worker(int r, int n, int workers) {
-  return (int)((((long long)r + 1) * workers - 1) / n);
+__device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float4* red, int warps) {
+  const int lane = threadIdx.x & 31;
+  float k = sum3_lanes(a, b, c, lane);
+  if (warps > 1) {
+    if ((lane & 7) == 0) reinterpret_cast<float*>(red + (threadIdx.x >> 5))[lane >> 3] = k;
+    __syncthreads();
+    const float4 v = lane < warps ? red[lane] : make_float4(0, 0, 0, 0);
+    k = sum3_lanes(v.x, v.y, v.z, lane);
+  }
+  a = __shfl_sync(0xffffffffu, k, 0);
+  b = __shfl_sync(0xffffffffu, k, 8);
+  c = __shfl_sync(0xffffffffu, k, 16);
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// One worker (block) owns a contiguous range of rows and walks it row by row;
-// a thread owns the same ITEMS chunks of columns in every row, so the sums
-// over tokens (dw_post, dw_next, dgate) stay in its registers until the range
-// or the gate's token group ends. STAGED: the next rows' chunks are on their
-// way into shared memory by cp.async while this one is computed; each thread
-// reads back only what it copied itself, so no barrier guards the ring.
-template <typename T, int VEC, int ITEMS, bool STAGED, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
+// Sums over tokens: dw_next in registers over all of the worker's rows; the
+// gate's and dw_post share one, A = sum D yr over the rows of one gate row,
+// of which they are dgate = b (w_post + off) A and dw_post += b gate A, taken
+// when the gate row or the range ends (dw_post's running sum waits in shared
+// memory between).
+template <typename T, int VEC, int EPT, bool STAGED, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
   extern __shared__ __align__(16) unsigned char nsm[];
-  __shared__ float red[2][3][32];
+  __shared__ float4 red[2][32];
   pdl_wait();
-  using C = Chunk<T, VEC>;
-  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warps = threads >> 5;
-  const int chunks = p.d / VEC;
+  constexpr int P = EPT / 2;
+  // with 64 registers a thread, y is read again for the second half of a row
+  constexpr bool KEEP_Y = MAXT * MINB <= 768;
+  const Cols<T, VEC, EPT> cols{(int)threadIdx.x, (int)blockDim.x, p.d / VEC};
+  const int warps = blockDim.x >> 5;
   const int w = blockIdx.x;
   const int r0 = worker_row(w, p.n, p.workers), r1 = worker_row(w + 1, p.n, p.workers);
   const T* dout = static_cast<const T*>(p.dout);
   const T* dh = static_cast<const T*>(p.dh);
   const T* out = static_cast<const T*>(p.out);
-  const T* y = static_cast<const T*>(p.y);
+  const T* gy = static_cast<const T*>(p.y);
   const T* gate = static_cast<const T*>(p.gate);
+  const bool gate_each = gate && p.gate_tokens == 1;
   const float inv_d = 1.0f / (float)p.d;
   const size_t row_bytes = (size_t)p.d * sizeof(T);
-  auto gate_row = [&](int r) {
-    return gate + (p.gate_tokens ? (long long)(r / p.gate_tokens) * p.gate_stride : 0);
-  };
+  // the ring, then dw_post's running sum [d] (fp32)
+  float* sum_post = reinterpret_cast<float*>(
+      nsm + (STAGED ? (size_t)p.stages * p.slots * row_bytes : 0));
+  // slots of a stage, in this order where present
+  const int s_out = 1, s_y = dh ? 2 : 0, s_dout = s_y + (gy ? 1 : 0),
+            s_gate = s_dout + (dout ? 1 : 0);
   auto issue = [&](int r) {
-    if (STAGED && r < r1) {
-      unsigned char* st = nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes;
-      const T* gr = gate ? gate_row(r) : nullptr;
-      const size_t base = (size_t)r * p.d;
+    if constexpr (STAGED) {
+      if (r < r1) {
+        unsigned char* st = nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes;
+        const size_t base = (size_t)r * p.d;
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const int c = i * threads + tid;
-        if (c < chunks) {
-          unsigned char* dst = st + (size_t)c * 16;
+        for (int i = 0; i < cols.ITEMS; ++i) {
+          if (!cols.has(i)) continue;
+          const int c = cols.at(i);
+          unsigned char* dst = st + (size_t)c * sizeof(T);
           if (dh) {
-            cp_async16(dst, dh + base + c * VEC), dst += row_bytes;
-            cp_async16(dst, out + base + c * VEC), dst += row_bytes;
+            cp_async16(dst, dh + base + c);
+            cp_async16(dst + s_out * row_bytes, out + base + c);
           }
-          if (y) cp_async16(dst, y + base + c * VEC), dst += row_bytes;
-          if (dout) cp_async16(dst, dout + base + c * VEC), dst += row_bytes;
-          if (gr) cp_async16(dst, gr + c * VEC);
+          if (gy) cp_async16(dst + s_y * row_bytes, gy + base + c);
+          if (dout) cp_async16(dst + s_dout * row_bytes, dout + base + c);
+          if (gate_each)
+            cp_async16(dst + s_gate * row_bytes, gate + (long long)r * p.gate_stride + c);
         }
       }
+      cp_async_commit();
     }
-    if (STAGED) cp_async_commit();
   };
-
-  float wp[ITEMS * VEC], wn[ITEMS * VEC];
-  float acc_p[ITEMS * VEC], acc_n[ITEMS * VEC], acc_g[ITEMS * VEC];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int c = i * threads + tid;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      wp[i * VEC + j] = 1.0f;
-      wn[i * VEC + j] = 0.0f;
-      acc_p[i * VEC + j] = acc_n[i * VEC + j] = acc_g[i * VEC + j] = 0.0f;
-    }
-    if (c < chunks) {
-      if (p.w_post) load_weights<VEC>(wp + i * VEC, p.w_post + c * VEC, p.off);
-      if (p.w_next) load_weights<VEC>(wn + i * VEC, p.w_next + c * VEC, p.off);
-    }
-  }
   for (int q = 0; q < p.stages - 1; ++q) issue(r0 + q);
+  float2 cw[P], wn[P], acc_n[P], A[P];
+#pragma unroll
+  for (int e = 0; e < P; ++e) cw[e] = wn[e] = acc_n[e] = A[e] = both(0.0f);
+  if (p.w_next) {
+    cols.load_f32(wn, p.w_next);
+#pragma unroll
+    for (int e = 0; e < P; ++e) wn[e] = add2(wn[e], both(p.off));
+  }
+  if (p.w_post) cols.store_f32(sum_post, A);
+  // w_post + off (1 without), and row r's gate (1 without)
+  auto post_weights = [&](float2* v) {
+    if (p.w_post) {
+      cols.load_f32(v, p.w_post);
+#pragma unroll
+      for (int e = 0; e < P; ++e) v[e] = add2(v[e], both(p.off));
+    } else {
+#pragma unroll
+      for (int e = 0; e < P; ++e) v[e] = both(1.0f);
+    }
+  };
+  auto gate_of = [&](float2* v, int r, const T* st) {
+    if (STAGED && gate_each)
+      cols.template load<true>(v, st + (size_t)s_gate * p.d);
+    else
+      cols.template load<false>(
+          v, gate + (p.gate_tokens ? (long long)(r / p.gate_tokens) * p.gate_stride : 0));
+  };
   for (int r = r0; r < r1; ++r) {
     issue(r + p.stages - 1);
     const size_t base = (size_t)r * p.d;
     const float rp = p.w_post ? p.rstd_post[r] : 1.0f;
     const float rn = dh ? p.rstd_next[r] : 0.0f;
-    if (STAGED) {
-      if (p.stages == 1) cp_async_wait<0>();
-      else if (p.stages == 2) cp_async_wait<1>();
-      else cp_async_wait<2>();
-    }
-    const unsigned char* st = nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes;
-    const T* gr = gate ? gate_row(r) : nullptr;
-    auto fetch = [&](int c, C& a_dh, C& a_out, C& a_y, C& a_dout, C& a_g) {
-      if (STAGED) {
-        const unsigned char* src = st + (size_t)c * 16;
-        if (dh) {
-          a_dh.load_smem(src), src += row_bytes;
-          a_out.load_smem(src), src += row_bytes;
-        }
-        if (y) a_y.load_smem(src), src += row_bytes;
-        if (dout) a_dout.load_smem(src), src += row_bytes;
-        if (gate) a_g.load_smem(src);
-      } else {
-        if (dh) {
-          a_dh.load(dh + base + c * VEC);
-          a_out.load(out + base + c * VEC);
-        }
-        if (y) a_y.load(y + base + c * VEC);
-        if (dout) a_dout.load(dout + base + c * VEC);
-        if (gate) a_g.load(gr + c * VEC);
+    if (STAGED) cp_async_wait_row(p.stages);
+    const T* st = reinterpret_cast<const T*>(
+        nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes);
+    if (gy && (r == r0 || (gate && p.gate_tokens && r % p.gate_tokens == 0))) {
+      post_weights(cw);
+#pragma unroll
+      for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], both(p.b));
+      if (gate) {
+        float2 g[P];
+        gate_of(g, r, st);
+#pragma unroll
+        for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], g[e]);
       }
-    };
-    // the three sums: q u, (dout + r2 q) c, u c
-    float s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+    }
+    // t = dout + r2 q, u = out r2; D = t - r2 mean(q u) u
+    float2 t[P], u[P], y[P];
+    if (dout) {
+      cols.template load<STAGED>(t, STAGED ? st + (size_t)s_dout * p.d : dout + base);
+    } else {
+#pragma unroll
+      for (int e = 0; e < P; ++e) t[e] = both(0.0f);
+    }
+    if (gy) cols.template load<STAGED>(y, STAGED ? st + (size_t)s_y * p.d : gy + base);
+    float k1 = 0.0f, k2 = 0.0f;
+    if (dh) {
+      float2 v[P];
+      cols.template load<STAGED>(u, STAGED ? st + (size_t)s_out * p.d : out + base);
+      cols.template load<STAGED>(v, STAGED ? st : dh + base);
+      float2 s1 = both(0.0f);
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        u[e] = mul2(u[e], both(rn));
+        acc_n[e] = fma2(v[e], u[e], acc_n[e]);
+        v[e] = mul2(v[e], wn[e]);
+        s1 = fma2(v[e], u[e], s1);
+        t[e] = fma2(v[e], both(rn), t[e]);
+      }
+      k1 = s1.x + s1.y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < P; ++e) u[e] = both(0.0f);
+    }
     if (dh || p.w_post) {
+      float2 s2 = both(0.0f), s3 = both(0.0f);
+      if (p.w_post) {
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const int c = i * threads + tid;
-        if (c < chunks) {
-          C a_dh, a_out, a_y, a_dout, a_g;
-          a_dh.zero();
-          a_out.zero();
-          a_y.zero();
-          a_dout.zero();
-          fetch(c, a_dh, a_out, a_y, a_dout, a_g);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const int e = i * VEC + j;
-            const float u = a_out.get(j) * rn;
-            const float q = a_dh.get(j) * wn[e];
-            float cc = a_y.get(j) * rp * wp[e];
-            if (gate) cc *= a_g.get(j);
-            s1 = fmaf(q, u, s1);
-            s2 = fmaf(fmaf(rn, q, a_dout.get(j)), cc, s2);
-            s3 = fmaf(u, cc, s3);
-            acc_n[e] = fmaf(a_dh.get(j), u, acc_n[e]);
-          }
+        for (int e = 0; e < P; ++e) {
+          const float2 c = mul2(y[e], cw[e]);
+          s2 = fma2(t[e], c, s2);
+          s3 = fma2(u[e], c, s3);
         }
       }
-      s1 = warp_sum(s1);
-      s2 = warp_sum(s2);
-      s3 = warp_sum(s3);
-      if (warps > 1) {
-        // two buffers: a warp may still read row r's while row r + 1 is written
-        float(*rd)[32] = red[r & 1];
-        if (lane == 0) {
-          rd[0][tid >> 5] = s1;
-          rd[1][tid >> 5] = s2;
-          rd[2][tid >> 5] = s3;
-        }
-        __syncthreads();
-        s1 = warp_sum(lane < warps ? rd[0][lane] : 0.0f);
-        s2 = warp_sum(lane < warps ? rd[1][lane] : 0.0f);
-        s3 = warp_sum(lane < warps ? rd[2][lane] : 0.0f);
-      }
+      float a2 = s2.x + s2.y, a3 = s3.x + s3.y;
+      // two buffers: a warp may still read row r's while row r + 1 is written
+      block_sum3(k1, a2, a3, red[r & 1], warps);
+      k1 *= rn * inv_d;                               // r2 mean(q u)
+      k2 = rp * rp * rp * (a2 - k1 * a3) * inv_d;     // r1^2 mean(D c)
     }
-    const float k1 = rn * s1 * inv_d;                  // r2 mean(q u)
-    const float m = p.b * (s2 - k1 * s3) * inv_d;      // mean(D c)
+    if (gy && !KEEP_Y) cols.template load<STAGED>(y, STAGED ? st + (size_t)s_y * p.d : gy + base);
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int c = i * threads + tid;
-      if (c < chunks) {
-        C a_dh, a_out, a_y, a_dout, a_g;
-        a_dh.zero();
-        a_out.zero();
-        a_y.zero();
-        a_dout.zero();
-        fetch(c, a_dh, a_out, a_y, a_dout, a_g);
-        float vx[VEC], vy[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const int e = i * VEC + j;
-          const float u = a_out.get(j) * rn;
-          const float q = a_dh.get(j) * wn[e];
-          const float D = fmaf(rn, q, a_dout.get(j)) - k1 * u;
-          vx[j] = p.a * D;
-          const float yr = a_y.get(j) * rp;
-          const float dz = p.b * D;
-          const float dv = gate ? dz * a_g.get(j) : dz;
-          acc_g[e] = fmaf(dz, yr * wp[e], acc_g[e]);
-          acc_p[e] = fmaf(dv, yr, acc_p[e]);
-          vy[j] = p.w_post ? rp * (dv * wp[e] - yr * m) : dv;
-        }
-        C::store(static_cast<T*>(p.dx) + base + c * VEC, vx);
-        if (y) C::store(static_cast<T*>(p.dy) + base + c * VEC, vy);
-      }
+    for (int e = 0; e < P; ++e) {
+      t[e] = fma2(u[e], both(-k1), t[e]);  // D
+      u[e] = mul2(t[e], both(p.a));
     }
-    if (gate && (r + 1 == r1 || (p.gate_tokens && (r + 1) % p.gate_tokens == 0))) {
-      const int g = p.gate_tokens ? r / p.gate_tokens : 0;
-      const long long first = (long long)g * p.gate_tokens;
-      const long long last = p.gate_tokens ? min(first + p.gate_tokens, (long long)p.n) : p.n;
-      float* part = nullptr;
-      if (first < r0) part = p.part_head + (size_t)w * p.pitch;
-      else if (last > r1) part = p.part_tail + (size_t)w * p.pitch;
-      T* dg = static_cast<T*>(p.dgate) + (long long)g * p.gate_stride;
+    cols.store(static_cast<T*>(p.dx) + base, u);
+    if (!gy) continue;
+    // without the norm, r1 is 1 and mean(D c) is left out
+    if (!p.w_post) k2 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const int c = i * threads + tid;
-        if (c < chunks) {
-          if (part) {
+    for (int e = 0; e < P; ++e) {
+      A[e] = fma2(t[e], mul2(y[e], both(rp)), A[e]);
+      u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(y[e], both(-k2)));
+    }
+    cols.store(static_cast<T*>(p.dy) + base, u);
+    if (r + 1 == r1 || (gate && p.gate_tokens && (r + 1) % p.gate_tokens == 0)) {
+      // the gate row, or the worker's range, ends
+      float2 g[P], wp[P];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) part[c * VEC + j] = acc_g[i * VEC + j];
-          } else {
-            C::store(dg + c * VEC, acc_g + i * VEC);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) acc_g[i * VEC + j] = 0.0f;
+      for (int e = 0; e < P; ++e) {
+        A[e] = mul2(A[e], both(p.b));
+        g[e] = both(1.0f);
       }
+      if (gate) {
+        gate_of(g, r, st);
+        post_weights(wp);
+#pragma unroll
+        for (int e = 0; e < P; ++e) wp[e] = mul2(wp[e], A[e]);
+        const int gi = p.gate_tokens ? r / p.gate_tokens : 0;
+        const long long first = (long long)gi * p.gate_tokens;
+        const long long last = p.gate_tokens ? min(first + p.gate_tokens, (long long)p.n) : p.n;
+        if (first < r0)
+          cols.store_f32(p.part_head + (size_t)w * p.pitch, wp);
+        else if (last > r1)
+          cols.store_f32(p.part_tail + (size_t)w * p.pitch, wp);
+        else
+          cols.store(static_cast<T*>(p.dgate) + (long long)gi * p.gate_stride, wp);
+      }
+      if (p.w_post) {
+        cols.load_f32(wp, sum_post);
+#pragma unroll
+        for (int e = 0; e < P; ++e) wp[e] = fma2(g[e], A[e], wp[e]);
+        cols.store_f32(sum_post, wp);
+      }
+#pragma unroll
+      for (int e = 0; e < P; ++e) A[e] = both(0.0f);
     }
   }
   const bool alone = p.workers == 1;
-  float* dst_p = alone ? p.dw_post : p.part_post + (size_t)w * p.pitch;
-  float* dst_n = alone ? p.dw_next : p.part_next + (size_t)w * p.pitch;
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int c = i * threads + tid;
-    if (c < chunks) {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (p.w_post) dst_p[c * VEC + j] = acc_p[i * VEC + j];
-        if (p.w_next) dst_n[c * VEC + j] = acc_n[i * VEC + j];
-      }
-    }
+  if (p.w_post) {
+    cols.load_f32(A, sum_post);
+    cols.store_f32(alone ? p.dw_post : p.part_post + (size_t)w * p.pitch, A);
   }
+  if (p.w_next) cols.store_f32(alone ? p.dw_next : p.part_next + (size_t)w * p.pitch, acc_n);
 }
 
-// Joins the workers' partial sums in worker order: 128 columns a block, 8
+// Joins the workers' partial sums in worker order: 128 columns a block, 32
 // slices of the workers, then the slices in order. blockIdx.y: dw_post,
 // dw_next, then the gate groups that more than one worker holds, found by
 // group (fewer groups than workers) or by the worker that they begin in.
@@ -521,7 +606,7 @@ struct NormReduce {
   NormBwd b;
   int by_group;
 };
-constexpr int kRedSlices = 8;
+constexpr int kRedSlices = 32;
 
 template <typename T>
 __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const NormReduce q) {
@@ -563,6 +648,7 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
   const int col = (blockIdx.x * 32 + threadIdx.x) * 4;
   float4 s = make_float4(0, 0, 0, 0);
   if (col < p.pitch) {
+#pragma unroll 4
     for (int w = w_lo + threadIdx.y; w < w_hi; w += kRedSlices) {
       const float* row = w == w_lo ? first_src : src + (size_t)w * p.pitch;
       const float4 v = *reinterpret_cast<const float4*>(row + col);
@@ -591,15 +677,15 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
   }
 }
 
-// ---- work split of the backward --------------------------------------------
-// Threads a worker: 8 elements each up to d = 8192, 16 above. Workers: about
-// 1024 threads an SM, and at least two rows each (fewer rows would only add
-// partial sums to join).
+// ---- work split of the backward ---------------------------------------------
+// At least two rows a worker: fewer would only add partial sums to join.
+// Workers an SM: what its registers hold (80 a thread up to 256 threads, 64
+// above).
 constexpr int kBwdMinRows = 2;
-int bwd_threads(int d) { return ((d <= 8192 ? (d + 7) / 8 : (d + 15) / 16) + 31) / 32 * 32; }
 int bwd_workers_per_sm(int d) {
-  const int k = 1024 / bwd_threads(d);
-  return k < 1 ? 1 : k > 12 ? 12 : k;
+  const int t = norm_threads(d);
+  const int k = (t <= 256 ? 768 : 1024) / t;
+  return k < 1 ? 1 : k > 16 ? 16 : k;
 }
 int bwd_workers(int n, int d) {
   const long long most = (long long)kBlockSms * bwd_workers_per_sm(d);
@@ -608,35 +694,39 @@ int bwd_workers(int n, int d) {
 }
 int bwd_pitch(int d) { return (d + 31) / 32 * 32; }
 
-template <typename T, int VEC, int ITEMS, bool STAGED, int MAXT>
-cudaError_t run_bwd(const NormBwd& p, int threads, size_t smem, cudaStream_t s) {
-  auto kern = norm_bwd_kernel<T, VEC, ITEMS, STAGED, MAXT>;
-  if (smem > 0) {
-    cudaError_t e =
+template <typename T, int VEC, int EPT, bool STAGED, int MAXT, int MINB>
+cudaError_t run_bwd(const NormBwd& p, size_t smem, cudaStream_t s) {
+  auto kern = norm_bwd_kernel<T, VEC, EPT, STAGED, MAXT, MINB>;
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kern, dim3(p.workers), dim3(threads), smem, s, p);
+  return launch_pdl(kern, dim3(p.workers), dim3(norm_threads(p.d)), smem, s, p);
 }
 
 template <typename T, int VEC>
 cudaError_t launch_bwd(NormBwd& p, bool vec, cudaStream_t s) {
-  const int threads = bwd_threads(p.d);
+  const int per_sm = bwd_workers_per_sm(p.d);
   const size_t row = (size_t)p.d * sizeof(T);
-  p.slots = (p.dh ? 2 : 0) + (p.y ? 1 : 0) + (p.dout ? 1 : 0) + (p.gate ? 1 : 0);
-  const size_t budget = (size_t)220 * 1024 / bwd_workers_per_sm(p.d) - 1024;
-  size_t st = budget / (p.slots * row);
-  p.stages = st > 3 ? 3 : (int)st;
-  const bool wide = p.d > 8192;
+  const size_t sums = p.w_post ? (size_t)p.d * 4 : 0;
+  p.slots = (p.dh ? 2 : 0) + (p.y ? 1 : 0) + (p.dout ? 1 : 0) +
+            (p.gate && p.gate_tokens == 1 ? 1 : 0);
+  const size_t budget = ring_budget(per_sm);
+  const size_t fit = budget > sums ? (budget - sums) / (p.slots * row) : 0;
+  const int deep = (p.n + p.workers - 1) / p.workers;
+  p.stages = fit > kMaxStages ? kMaxStages : (int)fit;
+  if (p.stages > deep) p.stages = deep;
   if (!vec || p.stages < 1) {
     p.stages = 1;
-    if (wide) return run_bwd<T, 1, 16, false, 1024>(p, threads, 0, s);
-    return run_bwd<T, 1, 8, false, 1024>(p, threads, 0, s);
+    return p.d > 8192 ? run_bwd<T, 1, 16, false, 1024, 1>(p, sums, s)
+                      : run_bwd<T, 1, 8, false, 1024, 1>(p, sums, s);
   }
-  const size_t smem = p.stages * p.slots * row;
-  if (wide) return run_bwd<T, VEC, 16 / VEC, true, 1024>(p, threads, smem, s);
-  if (threads > 512) return run_bwd<T, VEC, 8 / VEC, true, 1024>(p, threads, smem, s);
-  return run_bwd<T, VEC, 8 / VEC, true, 512>(p, threads, smem, s);
+  const size_t smem = p.stages * p.slots * row + sums;
+  if (p.d > 8192) return run_bwd<T, VEC, 16, true, 1024, 1>(p, smem, s);
+  const int threads = norm_threads(p.d);
+  if (threads <= 256) return run_bwd<T, VEC, 8, true, 256, 3>(p, smem, s);
+  return run_bwd<T, VEC, 8, true, 1024, 1>(p, smem, s);
 }
 
 moe_status norm_check(const moe_norm_config* c) {
@@ -688,11 +778,8 @@ moe_status forward_impl(const moe_norm_config* c, const NormFwd& q, cudaStream_t
     return MOE_ERR_INVALID_ARG;
   const bool vec =
       vectors(c, p.gate != nullptr, {p.x, p.y, p.gate, p.out, p.h, p.w_post, p.w_next});
-  cudaError_t e;
-  if (c->dtype == MOE_BF16)
-    e = vec ? launch_fwd<__nv_bfloat16, 8>(p, s) : launch_fwd<__nv_bfloat16, 1>(p, s);
-  else
-    e = vec ? launch_fwd<float, 4>(p, s) : launch_fwd<float, 1>(p, s);
+  const cudaError_t e = c->dtype == MOE_BF16 ? launch_fwd<__nv_bfloat16, 8>(p, vec, s)
+                                             : launch_fwd<float, 4>(p, vec, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -743,7 +830,7 @@ moe_status backward_impl(const moe_norm_config* c, const NormBwd& q, void* ws, s
   p.part_tail = p.part_head + each;
   const bool vec = vectors(c, p.gate != nullptr,
                            {p.dout, p.dh, p.out, p.y, p.gate, p.dx, p.dy, p.dgate, p.w_post,
-                            p.w_next});
+                            p.w_next, p.dw_post, p.dw_next});
   cudaError_t e = c->dtype == MOE_BF16 ? launch_bwd<__nv_bfloat16, 8>(p, vec, s)
                                        : launch_bwd<float, 4>(p, vec, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
