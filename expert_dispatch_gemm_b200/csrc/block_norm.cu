@@ -43,6 +43,18 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
+__device__ __forceinline__ uint32_t smem32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint4 load_smem16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(a)
+               : "memory");
+  return r;
+}
+
 // A thread's EPT elements of a row, as pairs: EPT / VEC chunks of VEC
 // neighbours, chunk c of the row at thread c % threads, so that an access of
 // the warp is one run of 16-byte vectors (VEC = 1: of single elements, for
@@ -55,8 +67,26 @@ struct Cols {
   __device__ __forceinline__ bool has(int i) const { return i * threads + tid < chunks; }
   __device__ __forceinline__ int at(int i) const { return (i * threads + tid) * VEC; }
 
-  // SMEM: a row that this thread copied itself; else global
-  template <bool SMEM>
+  static __device__ __forceinline__ void unpack(float2* o, const uint4& r) {
+    if constexpr (sizeof(T) == 4) {
+      o[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+      o[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+    } else {
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+    }
+  }
+  // from a staged row whose first byte is at shared address `a` (columns past
+  // d were zeroed there)
+  __device__ __forceinline__ void load_smem(float2* v, uint32_t a) const {
+    if constexpr (VEC > 1) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+        unpack(v + i * (VEC / 2), load_smem16(a + (uint32_t)(i * threads + tid) * 16));
+    }
+  }
   __device__ __forceinline__ void load(float2* v, const T* row) const {
     if constexpr (VEC == 1) {
 #pragma unroll
@@ -66,23 +96,9 @@ struct Cols {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (has(i)) {
-          const uint4* q = reinterpret_cast<const uint4*>(row + at(i));
-          r = SMEM ? *q : __ldcs(q);
-        }
-        float2* o = v + i * (VEC / 2);
-        if constexpr (sizeof(T) == 4) {
-          o[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
-          o[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
-        } else {
-          const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
-        }
-      }
+      for (int i = 0; i < ITEMS; ++i)
+        unpack(v + i * (VEC / 2), has(i) ? __ldcs(reinterpret_cast<const uint4*>(row + at(i)))
+                                         : make_uint4(0, 0, 0, 0));
     }
   }
   __device__ __forceinline__ void store(T* row, const float2* v) const {
@@ -146,10 +162,9 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
-               "l"(src)
+// 16 bytes, or (n = 0) zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
@@ -167,6 +182,16 @@ __device__ __forceinline__ void cp_async_wait_row(int stages) {
   else cp_async_wait<0>();
 }
 constexpr int kMaxStages = 4;
+
+// Shared addresses of a ring's next stage to fill and to read.
+struct Ring {
+  uint32_t first, bytes, end, fill, read;
+  __device__ __forceinline__ Ring(const void* smem, uint32_t stage_bytes, int stages)
+      : first(smem32(smem)), bytes(stage_bytes), end(first + stage_bytes * stages), fill(first),
+        read(first) {}
+  __device__ __forceinline__ void filled() { fill = fill + bytes == end ? first : fill + bytes; }
+  __device__ __forceinline__ void done() { read = read + bytes == end ? first : read + bytes; }
+};
 
 __host__ __device__ __forceinline__ int worker_row(int w, int n, int workers) {
   return (int)((long long)w * n / workers);
@@ -197,12 +222,12 @@ __device__ __forceinline__ float block_sum(float v, float* red, int warps) {
   const int lane = threadIdx.x & 31;
   if (lane == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  // (every lane of a group of 8, 16 or 32 holds one warp's sum)
-  const int group = warps <= 8 ? 8 : warps <= 16 ? 16 : 32;
-  const int i = lane & (group - 1);
-  v = i < warps ? red[i] : 0.0f;
-  for (int o = group / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  return warp_sum(lane < warps ? red[lane] : 0.0f);
+}
+
+// rows until the gate row of row r ends (a gate without groups never does)
+__device__ __forceinline__ int gate_rows_left(const void* gate, int tokens, int r) {
+  return gate && tokens ? tokens - r % tokens : 0x7fffffff;
 }
 
 template <typename T, int VEC, int EPT, bool STAGED>
@@ -213,88 +238,101 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p) {
   constexpr int P = EPT / 2;
   const Cols<T, VEC, EPT> cols{(int)threadIdx.x, (int)blockDim.x, p.d / VEC};
   const int warps = blockDim.x >> 5;
-  const int w = blockIdx.x;
-  const int r0 = worker_row(w, p.n, p.workers), r1 = worker_row(w + 1, p.n, p.workers);
-  const T* gx = static_cast<const T*>(p.x);
-  const T* gy = static_cast<const T*>(p.y);
+  const int r0 = worker_row(blockIdx.x, p.n, p.workers);
+  const int r1 = worker_row(blockIdx.x + 1, p.n, p.workers);
+  const bool has_y = p.y, post = p.w_post, next = p.h;
+  // this worker's rows; the filling pointers run ahead of `at` (elements)
+  const size_t base = (size_t)r0 * p.d;
+  const T* x = static_cast<const T*>(p.x) + base;
+  const T* y = static_cast<const T*>(p.y) + base;
+  T* out = static_cast<T*>(p.out) + base;
+  T* h = static_cast<T*>(p.h) + base;
   const T* gate = static_cast<const T*>(p.gate);
+  if (gate && p.gate_tokens) gate += (long long)(r0 / p.gate_tokens) * p.gate_stride;
   const bool gate_each = gate && p.gate_tokens == 1;  // its rows travel with the others
-  const size_t row_bytes = (size_t)p.d * sizeof(T);
+  const uint32_t pitch = (uint32_t)blockDim.x * EPT * sizeof(T);  // of a staged row
+  Ring ring(nsm, p.slots * pitch, p.stages);
   const float inv_d = 1.0f / (float)p.d;
-  auto issue = [&](int r) {
+  size_t fill_at = 0;
+  const T* fill_gate = gate;
+  int to_fill = r1 - r0;
+  auto issue = [&]() {
     if constexpr (STAGED) {
-      if (r < r1) {
-        unsigned char* st = nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes;
-        const size_t base = (size_t)r * p.d;
+      if (to_fill > 0) {
+        --to_fill;
 #pragma unroll
         for (int i = 0; i < cols.ITEMS; ++i) {
-          if (!cols.has(i)) continue;
-          unsigned char* dst = st + (size_t)cols.at(i) * sizeof(T);
-          cp_async16(dst, gx + base + cols.at(i));
-          if (gy) cp_async16(dst + row_bytes, gy + base + cols.at(i));
-          if (gate_each)
-            cp_async16(dst + 2 * row_bytes, gate + (long long)r * p.gate_stride + cols.at(i));
+          const uint32_t n = cols.has(i) ? 16 : 0;
+          const int c = n ? cols.at(i) : 0;
+          const uint32_t dst = ring.fill + (uint32_t)(i * cols.threads + cols.tid) * 16;
+          cp_async16(dst, x + fill_at + c, n);
+          if (has_y) cp_async16(dst + pitch, y + fill_at + c, n);
+          if (gate_each) cp_async16(dst + 2 * pitch, fill_gate + c, n);
         }
+        fill_at += p.d;
+        fill_gate += p.gate_stride;
+        ring.filled();
       }
       cp_async_commit();
     }
   };
-  for (int q = 0; q < p.stages - 1; ++q) issue(r0 + q);
+  for (int q = 0; q < p.stages - 1; ++q) issue();
   float2 cw[P], wn[P];  // b gate (w_post + off); w_next + off
-  if (p.h) {
+  if (next) {
     cols.load_f32(wn, p.w_next);
 #pragma unroll
     for (int e = 0; e < P; ++e) wn[e] = add2(wn[e], both(p.off));
   }
-  for (int r = r0; r < r1; ++r) {
-    issue(r + p.stages - 1);
+  int left = 0;  // rows for which cw holds
+  size_t at = 0;
+  for (int r = r0; r < r1; ++r, at += p.d) {
+    issue();
     if (STAGED) cp_async_wait_row(p.stages);
-    const size_t base = (size_t)r * p.d;
-    const T* st = reinterpret_cast<const T*>(
-        nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes);
-    if (gy && (r == r0 || (gate && p.gate_tokens && r % p.gate_tokens == 0))) {
-      if (p.w_post) {
-        cols.load_f32(cw, p.w_post);
-#pragma unroll
-        for (int e = 0; e < P; ++e) cw[e] = mul2(add2(cw[e], both(p.off)), both(p.b));
-      } else {
-#pragma unroll
-        for (int e = 0; e < P; ++e) cw[e] = both(p.b);
-      }
-      if (gate) {
-        float2 g[P];
-        if (STAGED && gate_each)
-          cols.template load<true>(g, st + 2 * p.d);
-        else
-          cols.template load<false>(
-              g, gate + (p.gate_tokens ? (long long)(r / p.gate_tokens) * p.gate_stride : 0));
-#pragma unroll
-        for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], g[e]);
-      }
-    }
     float2 o[P];
-    if (gy) {
-      float2 y[P];
-      cols.template load<STAGED>(y, STAGED ? st + p.d : gy + base);
-      if (!STAGED) cols.template load<false>(o, gx + base);
+    if (has_y) {
+      if (left == 0) {
+        if (post) {
+          cols.load_f32(cw, p.w_post);
+#pragma unroll
+          for (int e = 0; e < P; ++e) cw[e] = mul2(add2(cw[e], both(p.off)), both(p.b));
+        } else {
+#pragma unroll
+          for (int e = 0; e < P; ++e) cw[e] = both(p.b);
+        }
+        if (gate) {
+          float2 g[P];
+          if (STAGED && gate_each) cols.load_smem(g, ring.read + 2 * pitch);
+          else cols.load(g, gate);
+          gate += p.gate_stride;
+#pragma unroll
+          for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], g[e]);
+        }
+        left = gate_rows_left(p.gate, p.gate_tokens, r);
+      }
+      --left;
+      float2 v[P];
+      if (STAGED) cols.load_smem(v, ring.read + pitch);
+      else cols.load(v, y + at), cols.load(o, x + at);
       float rp = 1.0f;
-      if (p.w_post) {
+      if (post) {
         float2 s = both(0.0f);
 #pragma unroll
-        for (int e = 0; e < P; ++e) s = fma2(y[e], y[e], s);
+        for (int e = 0; e < P; ++e) s = fma2(v[e], v[e], s);
         const float ss = block_sum(s.x + s.y, red[r & 1][0], warps);
         rp = rsqrtf(ss * inv_d + p.eps);
         if (p.rstd_post && threadIdx.x == 0) p.rstd_post[r] = rp;
       }
-      if (STAGED) cols.template load<true>(o, st);
+      if (STAGED) cols.load_smem(o, ring.read);
 #pragma unroll
       for (int e = 0; e < P; ++e)
-        o[e] = fma2(mul2(y[e], cw[e]), both(rp), mul2(o[e], both(p.a)));
-      cols.store(static_cast<T*>(p.out) + base, o);
+        o[e] = fma2(mul2(v[e], cw[e]), both(rp), mul2(o[e], both(p.a)));
+      cols.store(out + at, o);
+    } else if (STAGED) {
+      cols.load_smem(o, ring.read);
     } else {
-      cols.template load<STAGED>(o, STAGED ? st : gx + base);
+      cols.load(o, x + at);
     }
-    if (p.h) {
+    if (next) {
       float2 s = both(0.0f);
 #pragma unroll
       for (int e = 0; e < P; ++e) s = fma2(o[e], o[e], s);
@@ -303,8 +341,9 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p) {
       if (p.rstd_next && threadIdx.x == 0) p.rstd_next[r] = rn;
 #pragma unroll
       for (int e = 0; e < P; ++e) o[e] = mul2(mul2(o[e], both(rn)), wn[e]);
-      cols.store(static_cast<T*>(p.h) + base, o);
+      cols.store(h + at, o);
     }
+    ring.done();
   }
 }
 
@@ -336,7 +375,7 @@ cudaError_t launch_fwd(NormFwd& p, bool vec, cudaStream_t s) {
   const long long most = (long long)kBlockSms * per_sm;
   p.workers = (int)(p.n < most ? p.n : most);
   p.slots = p.gate && p.gate_tokens == 1 ? 3 : p.y ? 2 : 1;
-  const size_t row = (size_t)p.d * sizeof(T);
+  const size_t row = (size_t)norm_threads(p.d) * (p.d > 8192 ? 16 : 8) * sizeof(T);
   const size_t fit = ring_budget(per_sm) / (p.slots * row);
   const int deep = (p.n + p.workers - 1) / p.workers;  // no more stages than rows
   p.stages = fit > kMaxStages ? kMaxStages : (int)fit;
@@ -413,56 +452,66 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
   const int warps = blockDim.x >> 5;
   const int w = blockIdx.x;
   const int r0 = worker_row(w, p.n, p.workers), r1 = worker_row(w + 1, p.n, p.workers);
-  const T* dout = static_cast<const T*>(p.dout);
-  const T* dh = static_cast<const T*>(p.dh);
-  const T* out = static_cast<const T*>(p.out);
-  const T* gy = static_cast<const T*>(p.y);
+  const bool has_y = p.y, post = p.w_post, next = p.dh, has_dout = p.dout;
+  const size_t base = (size_t)r0 * p.d;
+  const T* dout = static_cast<const T*>(p.dout) + base;
+  const T* dh = static_cast<const T*>(p.dh) + base;
+  const T* out = static_cast<const T*>(p.out) + base;
+  const T* y = static_cast<const T*>(p.y) + base;
+  T* dx = static_cast<T*>(p.dx) + base;
+  T* dy = static_cast<T*>(p.dy) + base;
   const T* gate = static_cast<const T*>(p.gate);
+  if (gate && p.gate_tokens) gate += (long long)(r0 / p.gate_tokens) * p.gate_stride;
   const bool gate_each = gate && p.gate_tokens == 1;
   const float inv_d = 1.0f / (float)p.d;
-  const size_t row_bytes = (size_t)p.d * sizeof(T);
-  // the ring, then dw_post's running sum [d] (fp32)
-  float* sum_post = reinterpret_cast<float*>(
-      nsm + (STAGED ? (size_t)p.stages * p.slots * row_bytes : 0));
-  // slots of a stage, in this order where present
-  const int s_out = 1, s_y = dh ? 2 : 0, s_dout = s_y + (gy ? 1 : 0),
-            s_gate = s_dout + (dout ? 1 : 0);
-  auto issue = [&](int r) {
+  // the ring, then dw_post's running sum [columns] (fp32)
+  const uint32_t pitch = (uint32_t)blockDim.x * EPT * sizeof(T);
+  Ring ring(nsm, p.slots * pitch, p.stages);
+  float* sum_post =
+      reinterpret_cast<float*>(nsm + (STAGED ? (size_t)p.stages * p.slots * pitch : 0));
+  // offsets of a stage's rows, in this order where present: dh, out, y, dout, gate
+  const uint32_t s_y = next ? 2 * pitch : 0, s_dout = s_y + (has_y ? pitch : 0),
+                 s_gate = s_dout + (has_dout ? pitch : 0);
+  size_t fill_at = 0;
+  const T* fill_gate = gate;
+  int to_fill = r1 - r0;
+  auto issue = [&]() {
     if constexpr (STAGED) {
-      if (r < r1) {
-        unsigned char* st = nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes;
-        const size_t base = (size_t)r * p.d;
+      if (to_fill > 0) {
+        --to_fill;
 #pragma unroll
         for (int i = 0; i < cols.ITEMS; ++i) {
-          if (!cols.has(i)) continue;
-          const int c = cols.at(i);
-          unsigned char* dst = st + (size_t)c * sizeof(T);
-          if (dh) {
-            cp_async16(dst, dh + base + c);
-            cp_async16(dst + s_out * row_bytes, out + base + c);
+          const uint32_t n = cols.has(i) ? 16 : 0;
+          const size_t c = fill_at + (n ? cols.at(i) : 0);
+          const uint32_t dst = ring.fill + (uint32_t)(i * cols.threads + cols.tid) * 16;
+          if (next) {
+            cp_async16(dst, dh + c, n);
+            cp_async16(dst + pitch, out + c, n);
           }
-          if (gy) cp_async16(dst + s_y * row_bytes, gy + base + c);
-          if (dout) cp_async16(dst + s_dout * row_bytes, dout + base + c);
-          if (gate_each)
-            cp_async16(dst + s_gate * row_bytes, gate + (long long)r * p.gate_stride + c);
+          if (has_y) cp_async16(dst + s_y, y + c, n);
+          if (has_dout) cp_async16(dst + s_dout, dout + c, n);
+          if (gate_each) cp_async16(dst + s_gate, fill_gate + (n ? cols.at(i) : 0), n);
         }
+        fill_at += p.d;
+        fill_gate += p.gate_stride;
+        ring.filled();
       }
       cp_async_commit();
     }
   };
-  for (int q = 0; q < p.stages - 1; ++q) issue(r0 + q);
+  for (int q = 0; q < p.stages - 1; ++q) issue();
   float2 cw[P], wn[P], acc_n[P], A[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) cw[e] = wn[e] = acc_n[e] = A[e] = both(0.0f);
-  if (p.w_next) {
+  if (next) {
     cols.load_f32(wn, p.w_next);
 #pragma unroll
     for (int e = 0; e < P; ++e) wn[e] = add2(wn[e], both(p.off));
   }
-  if (p.w_post) cols.store_f32(sum_post, A);
-  // w_post + off (1 without), and row r's gate (1 without)
+  if (post) cols.store_f32(sum_post, A);
+  // w_post + off (1 without)
   auto post_weights = [&](float2* v) {
-    if (p.w_post) {
+    if (post) {
       cols.load_f32(v, p.w_post);
 #pragma unroll
       for (int e = 0; e < P; ++e) v[e] = add2(v[e], both(p.off));
@@ -471,46 +520,43 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
       for (int e = 0; e < P; ++e) v[e] = both(1.0f);
     }
   };
-  auto gate_of = [&](float2* v, int r, const T* st) {
-    if (STAGED && gate_each)
-      cols.template load<true>(v, st + (size_t)s_gate * p.d);
-    else
-      cols.template load<false>(
-          v, gate + (p.gate_tokens ? (long long)(r / p.gate_tokens) * p.gate_stride : 0));
+  auto gate_row = [&](float2* v) {
+    if (STAGED && gate_each) cols.load_smem(v, ring.read + s_gate);
+    else cols.load(v, gate);
   };
-  for (int r = r0; r < r1; ++r) {
-    issue(r + p.stages - 1);
-    const size_t base = (size_t)r * p.d;
-    const float rp = p.w_post ? p.rstd_post[r] : 1.0f;
-    const float rn = dh ? p.rstd_next[r] : 0.0f;
+  int left = 0;
+  size_t at = 0;
+  for (int r = r0; r < r1; ++r, at += p.d) {
+    issue();
+    const float rp = post ? p.rstd_post[r] : 1.0f;
+    const float rn = next ? p.rstd_next[r] : 0.0f;
     if (STAGED) cp_async_wait_row(p.stages);
-    const T* st = reinterpret_cast<const T*>(
-        nsm + (size_t)((r - r0) % p.stages) * p.slots * row_bytes);
-    if (gy && (r == r0 || (gate && p.gate_tokens && r % p.gate_tokens == 0))) {
+    if (left == 0 && has_y) {
       post_weights(cw);
 #pragma unroll
       for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], both(p.b));
       if (gate) {
         float2 g[P];
-        gate_of(g, r, st);
+        gate_row(g);
 #pragma unroll
         for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], g[e]);
       }
+      left = gate_rows_left(gate, p.gate_tokens, r);
     }
+    --left;
     // t = dout + r2 q, u = out r2; D = t - r2 mean(q u) u
-    float2 t[P], u[P], y[P];
-    if (dout) {
-      cols.template load<STAGED>(t, STAGED ? st + (size_t)s_dout * p.d : dout + base);
+    float2 t[P], u[P], v[P];
+    if (has_dout) {
+      if (STAGED) cols.load_smem(t, ring.read + s_dout);
+      else cols.load(t, dout + at);
     } else {
 #pragma unroll
       for (int e = 0; e < P; ++e) t[e] = both(0.0f);
     }
-    if (gy) cols.template load<STAGED>(y, STAGED ? st + (size_t)s_y * p.d : gy + base);
     float k1 = 0.0f, k2 = 0.0f;
-    if (dh) {
-      float2 v[P];
-      cols.template load<STAGED>(u, STAGED ? st + (size_t)s_out * p.d : out + base);
-      cols.template load<STAGED>(v, STAGED ? st : dh + base);
+    if (next) {
+      if (STAGED) cols.load_smem(u, ring.read + pitch), cols.load_smem(v, ring.read);
+      else cols.load(u, out + at), cols.load(v, dh + at);
       float2 s1 = both(0.0f);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -525,12 +571,17 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
 #pragma unroll
       for (int e = 0; e < P; ++e) u[e] = both(0.0f);
     }
-    if (dh || p.w_post) {
+    auto load_y = [&]() {
+      if (STAGED) cols.load_smem(v, ring.read + s_y);
+      else cols.load(v, y + at);
+    };
+    if (has_y) load_y();
+    if (next || post) {
       float2 s2 = both(0.0f), s3 = both(0.0f);
-      if (p.w_post) {
+      if (post) {
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-          const float2 c = mul2(y[e], cw[e]);
+          const float2 c = mul2(v[e], cw[e]);
           s2 = fma2(t[e], c, s2);
           s3 = fma2(u[e], c, s3);
         }
@@ -538,57 +589,58 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
       float a2 = s2.x + s2.y, a3 = s3.x + s3.y;
       // two buffers: a warp may still read row r's while row r + 1 is written
       block_sum3(k1, a2, a3, red[r & 1], warps);
-      k1 *= rn * inv_d;                               // r2 mean(q u)
-      k2 = rp * rp * rp * (a2 - k1 * a3) * inv_d;     // r1^2 mean(D c)
+      k1 *= rn * inv_d;                            // r2 mean(q u)
+      k2 = rp * rp * rp * (a2 - k1 * a3) * inv_d;  // r1^2 mean(D c); 0 without the norm
+      if (has_y && !KEEP_Y) load_y();
     }
-    if (gy && !KEEP_Y) cols.template load<STAGED>(y, STAGED ? st + (size_t)s_y * p.d : gy + base);
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       t[e] = fma2(u[e], both(-k1), t[e]);  // D
       u[e] = mul2(t[e], both(p.a));
     }
-    cols.store(static_cast<T*>(p.dx) + base, u);
-    if (!gy) continue;
-    // without the norm, r1 is 1 and mean(D c) is left out
-    if (!p.w_post) k2 = 0.0f;
-#pragma unroll
-    for (int e = 0; e < P; ++e) {
-      A[e] = fma2(t[e], mul2(y[e], both(rp)), A[e]);
-      u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(y[e], both(-k2)));
-    }
-    cols.store(static_cast<T*>(p.dy) + base, u);
-    if (r + 1 == r1 || (gate && p.gate_tokens && (r + 1) % p.gate_tokens == 0)) {
-      // the gate row, or the worker's range, ends
-      float2 g[P], wp[P];
+    cols.store(dx + at, u);
+    if (has_y) {
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        A[e] = mul2(A[e], both(p.b));
-        g[e] = both(1.0f);
+        A[e] = fma2(t[e], mul2(v[e], both(rp)), A[e]);
+        u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(v[e], both(-k2)));
       }
-      if (gate) {
-        gate_of(g, r, st);
-        post_weights(wp);
+      cols.store(dy + at, u);
+      if (left == 0 || r + 1 == r1) {
+        // the gate row, or the worker's range, ends
+        float2 g[P], wp[P];
 #pragma unroll
-        for (int e = 0; e < P; ++e) wp[e] = mul2(wp[e], A[e]);
-        const int gi = p.gate_tokens ? r / p.gate_tokens : 0;
-        const long long first = (long long)gi * p.gate_tokens;
-        const long long last = p.gate_tokens ? min(first + p.gate_tokens, (long long)p.n) : p.n;
-        if (first < r0)
-          cols.store_f32(p.part_head + (size_t)w * p.pitch, wp);
-        else if (last > r1)
-          cols.store_f32(p.part_tail + (size_t)w * p.pitch, wp);
-        else
-          cols.store(static_cast<T*>(p.dgate) + (long long)gi * p.gate_stride, wp);
+        for (int e = 0; e < P; ++e) {
+          A[e] = mul2(A[e], both(p.b));
+          g[e] = both(1.0f);
+        }
+        if (gate) {
+          gate_row(g);
+          gate += p.gate_tokens ? p.gate_stride : 0;
+          post_weights(wp);
+#pragma unroll
+          for (int e = 0; e < P; ++e) wp[e] = mul2(wp[e], A[e]);
+          const int gi = p.gate_tokens ? r / p.gate_tokens : 0;
+          const long long first = (long long)gi * p.gate_tokens;
+          const long long last = p.gate_tokens ? min(first + p.gate_tokens, (long long)p.n) : p.n;
+          if (first < r0)
+            cols.store_f32(p.part_head + (size_t)w * p.pitch, wp);
+          else if (last > r1)
+            cols.store_f32(p.part_tail + (size_t)w * p.pitch, wp);
+          else
+            cols.store(static_cast<T*>(p.dgate) + (long long)gi * p.gate_stride, wp);
+        }
+        if (post) {
+          cols.load_f32(wp, sum_post);
+#pragma unroll
+          for (int e = 0; e < P; ++e) wp[e] = fma2(g[e], A[e], wp[e]);
+          cols.store_f32(sum_post, wp);
+        }
+#pragma unroll
+        for (int e = 0; e < P; ++e) A[e] = both(0.0f);
       }
-      if (p.w_post) {
-        cols.load_f32(wp, sum_post);
-#pragma unroll
-        for (int e = 0; e < P; ++e) wp[e] = fma2(g[e], A[e], wp[e]);
-        cols.store_f32(sum_post, wp);
-      }
-#pragma unroll
-      for (int e = 0; e < P; ++e) A[e] = both(0.0f);
     }
+    ring.done();
   }
   const bool alone = p.workers == 1;
   if (p.w_post) {
@@ -708,7 +760,7 @@ cudaError_t run_bwd(const NormBwd& p, size_t smem, cudaStream_t s) {
 template <typename T, int VEC>
 cudaError_t launch_bwd(NormBwd& p, bool vec, cudaStream_t s) {
   const int per_sm = bwd_workers_per_sm(p.d);
-  const size_t row = (size_t)p.d * sizeof(T);
+  const size_t row = (size_t)norm_threads(p.d) * (p.d > 8192 ? 16 : 8) * sizeof(T);
   const size_t sums = p.w_post ? (size_t)p.d * 4 : 0;
   p.slots = (p.dh ? 2 : 0) + (p.y ? 1 : 0) + (p.dout ? 1 : 0) +
             (p.gate && p.gate_tokens == 1 ? 1 : 0);
