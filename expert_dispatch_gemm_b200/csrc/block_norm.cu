@@ -361,7 +361,7 @@ int fwd_workers_per_sm(int d) {
 template <typename T, int VEC, int EPT, bool STAGED>
 cudaError_t run_fwd(const NormFwd& p, size_t smem, cudaStream_t s) {
   auto kern = norm_fwd_kernel<T, VEC, EPT, STAGED>;
-  if (smem > 48 * 1024) {
+  if (smem > 32 * 1024) {  // (48 KB with the static part need no leave)
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -395,18 +395,20 @@ struct NormBwd {
   const void *dout, *dh, *out, *y, *gate;
   const float *w_post, *w_next, *rstd_post, *rstd_next;
   void *dx, *dy, *dgate;
-  float *dw_post, *dw_next;  // final sums (workers == 1)
-  // partial sums: [workers][pitch] each; a worker's incomplete gate groups
-  // are the one that began in an earlier worker (head) and the one that goes
-  // on in a later one (tail)
-  float *part_post, *part_next, *part_head, *part_tail;
+  float *dw_post, *dw_next;
+  // partial sums [blocks][pitch] of dw_post, dw_next and, with one gate row
+  // for all tokens, of dgate; with more gate rows [workers][pitch] of the
+  // rows that a worker holds a part of: the one that began in an earlier
+  // worker (head) and the one that goes on in a later one (tail)
+  float *part_post, *part_next, *part_gate, *part_head, *part_tail;
   int pitch;
-  int n, d, gate_tokens, workers, stages, slots;
+  int n, d, gate_tokens, workers, blocks, stages, slots;
+  uint32_t ring_bytes;  // of a worker
   float off, a, b;
   long long gate_stride;
 };
 
-// Three sums over the block at once. Within a warp, halves of the lanes first
+// Three sums over a worker at once. Within a warp, halves of the lanes first
 // trade values so that each lane carries one sum (18 instructions instead of
 // 30); the warps' sums then meet in `red` as one 16-byte vector a warp.
 __device__ __forceinline__ float sum3_lanes(float a, float b, float c, int lane) {
@@ -421,12 +423,13 @@ __device__ __forceinline__ float sum3_lanes(float a, float b, float c, int lane)
   k += __shfl_xor_sync(0xffffffffu, k, 1);
   return k;  // lanes 0-7: a, 8-15: b, 16-23: c
 }
-__device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float4* red, int warps) {
+// (red: the worker's, one entry a warp; a worker's barrier is its own)
+__device__ __forceinline__ void worker_sum3(float& a, float& b, float& c, float4* red, int warps) {
   const int lane = threadIdx.x & 31;
   float k = sum3_lanes(a, b, c, lane);
   if (warps > 1) {
     if ((lane & 7) == 0) reinterpret_cast<float*>(red + (threadIdx.x >> 5))[lane >> 3] = k;
-    __syncthreads();
+    asm volatile("bar.sync %0, %1;" ::"r"(threadIdx.y + 1), "r"(warps * 32) : "memory");
     const float4 v = lane < warps ? red[lane] : make_float4(0, 0, 0, 0);
     k = sum3_lanes(v.x, v.y, v.z, lane);
   }
@@ -435,71 +438,73 @@ __device__ __forceinline__ void block_sum3(float& a, float& b, float& c, float4*
   c = __shfl_sync(0xffffffffu, k, 16);
 }
 
+// A block holds blockDim.y workers of blockDim.x threads, each with rows, ring
+// and barrier of its own; at the end their sums meet in shared memory, so that
+// a block leaves one partial row.
 // Sums over tokens: dw_next in registers over all of the worker's rows; the
 // gate's and dw_post share one, A = sum D yr over the rows of one gate row,
 // of which they are dgate = b (w_post + off) A and dw_post += b gate A, taken
 // when the gate row or the range ends (dw_post's running sum waits in shared
 // memory between).
-template <typename T, int VEC, int EPT, bool STAGED, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
+template <typename T, int VEC, int EPT, bool STAGED, int MAXT, bool ALL>
+__global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
   extern __shared__ __align__(16) unsigned char nsm[];
   __shared__ float4 red[2][32];
   pdl_wait();
   constexpr int P = EPT / 2;
   // with 64 registers a thread, y is read again for the second half of a row
-  constexpr bool KEEP_Y = MAXT * MINB <= 768;
+  constexpr bool KEEP_Y = MAXT <= 768;
   const Cols<T, VEC, EPT> cols{(int)threadIdx.x, (int)blockDim.x, p.d / VEC};
   const int warps = blockDim.x >> 5;
-  const int w = blockIdx.x;
-  const int r0 = worker_row(w, p.n, p.workers), r1 = worker_row(w + 1, p.n, p.workers);
-  const bool has_y = p.y, post = p.w_post, next = p.dh, has_dout = p.dout;
-  const size_t base = (size_t)r0 * p.d;
-  const T* dout = static_cast<const T*>(p.dout) + base;
-  const T* dh = static_cast<const T*>(p.dh) + base;
-  const T* out = static_cast<const T*>(p.out) + base;
-  const T* y = static_cast<const T*>(p.y) + base;
-  T* dx = static_cast<T*>(p.dx) + base;
-  T* dy = static_cast<T*>(p.dy) + base;
-  const T* gate = static_cast<const T*>(p.gate);
-  if (gate && p.gate_tokens) gate += (long long)(r0 / p.gate_tokens) * p.gate_stride;
-  const bool gate_each = gate && p.gate_tokens == 1;
+  const int group = threadIdx.y, groups = blockDim.y;
+  const int w = blockIdx.x * groups + group;
+  const int r0 = w < p.workers ? worker_row(w, p.n, p.workers) : p.n;
+  const int r1 = w < p.workers ? worker_row(w + 1, p.n, p.workers) : p.n;
+  // ALL: every optional part but the gate is there, known when compiled (it
+  // saves the registers of the other kernel's flags)
+  const bool has_y = ALL || p.y, post = ALL || p.w_post, next = ALL || p.dh,
+             has_dout = ALL || p.dout;
+  const bool gate_all = p.gate && p.gate_tokens == 0, gate_each = p.gate && p.gate_tokens == 1;
+  // (addresses are made from the parameters and one offset: registers are short)
+  auto in = [](const void* q, size_t at) { return static_cast<const T*>(q) + at; };
+  auto to = [](void* q, size_t at) { return static_cast<T*>(q) + at; };
   const float inv_d = 1.0f / (float)p.d;
-  // the ring, then dw_post's running sum [columns] (fp32)
+  // the workers' rings; each takes the sums of dw_next and of the one gate row
+  // at its worker's end; then the running sums of dw_post (fp32, [columns] each)
   const uint32_t pitch = (uint32_t)blockDim.x * EPT * sizeof(T);
-  Ring ring(nsm, p.slots * pitch, p.stages);
+  const uint32_t fpitch = (uint32_t)blockDim.x * EPT;
+  unsigned char* mine = nsm + (size_t)group * p.ring_bytes;
+  Ring ring(mine, p.slots * pitch, p.stages);
+  float* end_next = reinterpret_cast<float*>(mine);
+  float* end_gate = end_next + (next ? fpitch : 0);
   float* sum_post =
-      reinterpret_cast<float*>(nsm + (STAGED ? (size_t)p.stages * p.slots * pitch : 0));
+      reinterpret_cast<float*>(nsm + (size_t)groups * p.ring_bytes) + (size_t)group * fpitch;
   // offsets of a stage's rows, in this order where present: dh, out, y, dout, gate
   const uint32_t s_y = next ? 2 * pitch : 0, s_dout = s_y + (has_y ? pitch : 0),
                  s_gate = s_dout + (has_dout ? pitch : 0);
-  size_t fill_at = 0;
-  const T* fill_gate = gate;
-  int to_fill = r1 - r0;
-  auto issue = [&]() {
+  auto issue = [&](int r) {
     if constexpr (STAGED) {
-      if (to_fill > 0) {
-        --to_fill;
+      if (r < r1) {
+        const size_t row = (size_t)r * p.d;
 #pragma unroll
         for (int i = 0; i < cols.ITEMS; ++i) {
           const uint32_t n = cols.has(i) ? 16 : 0;
-          const size_t c = fill_at + (n ? cols.at(i) : 0);
+          const int c = n ? cols.at(i) : 0;
           const uint32_t dst = ring.fill + (uint32_t)(i * cols.threads + cols.tid) * 16;
           if (next) {
-            cp_async16(dst, dh + c, n);
-            cp_async16(dst + pitch, out + c, n);
+            cp_async16(dst, in(p.dh, row + c), n);
+            cp_async16(dst + pitch, in(p.out, row + c), n);
           }
-          if (has_y) cp_async16(dst + s_y, y + c, n);
-          if (has_dout) cp_async16(dst + s_dout, dout + c, n);
-          if (gate_each) cp_async16(dst + s_gate, fill_gate + (n ? cols.at(i) : 0), n);
+          if (has_y) cp_async16(dst + s_y, in(p.y, row + c), n);
+          if (has_dout) cp_async16(dst + s_dout, in(p.dout, row + c), n);
+          if (gate_each) cp_async16(dst + s_gate, in(p.gate, r * p.gate_stride + c), n);
         }
-        fill_at += p.d;
-        fill_gate += p.gate_stride;
         ring.filled();
       }
       cp_async_commit();
     }
   };
-  for (int q = 0; q < p.stages - 1; ++q) issue();
+  for (int q = 0; q < p.stages - 1; ++q) issue(r0 + q);
   float2 cw[P], wn[P], acc_n[P], A[P];
 #pragma unroll
   for (int e = 0; e < P; ++e) cw[e] = wn[e] = acc_n[e] = A[e] = both(0.0f);
@@ -520,35 +525,40 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
       for (int e = 0; e < P; ++e) v[e] = both(1.0f);
     }
   };
-  auto gate_row = [&](float2* v) {
+  auto gate_row = [&](float2* v, int r) {
     if (STAGED && gate_each) cols.load_smem(v, ring.read + s_gate);
-    else cols.load(v, gate);
+    else cols.load(v, in(p.gate, p.gate_tokens ? r / p.gate_tokens * p.gate_stride : 0));
   };
   int left = 0;
-  size_t at = 0;
-  for (int r = r0; r < r1; ++r, at += p.d) {
-    issue();
-    const float rp = post ? p.rstd_post[r] : 1.0f;
-    const float rn = next ? p.rstd_next[r] : 0.0f;
+  float rp_ahead = post && r0 < r1 ? p.rstd_post[r0] : 1.0f;
+  float rn_ahead = next && r0 < r1 ? p.rstd_next[r0] : 0.0f;
+  for (int r = r0; r < r1; ++r) {
+    issue(r + p.stages - 1);
+    const size_t at = (size_t)r * p.d;
+    const float rp = rp_ahead, rn = rn_ahead;
+    if (r + 1 < r1) {
+      if (post) rp_ahead = p.rstd_post[r + 1];
+      if (next) rn_ahead = p.rstd_next[r + 1];
+    }
     if (STAGED) cp_async_wait_row(p.stages);
     if (left == 0 && has_y) {
       post_weights(cw);
 #pragma unroll
       for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], both(p.b));
-      if (gate) {
+      if (p.gate) {
         float2 g[P];
-        gate_row(g);
+        gate_row(g, r);
 #pragma unroll
         for (int e = 0; e < P; ++e) cw[e] = mul2(cw[e], g[e]);
       }
-      left = gate_rows_left(gate, p.gate_tokens, r);
+      left = gate_rows_left(p.gate, p.gate_tokens, r);
     }
     --left;
     // t = dout + r2 q, u = out r2; D = t - r2 mean(q u) u
     float2 t[P], u[P], v[P];
     if (has_dout) {
       if (STAGED) cols.load_smem(t, ring.read + s_dout);
-      else cols.load(t, dout + at);
+      else cols.load(t, in(p.dout, at));
     } else {
 #pragma unroll
       for (int e = 0; e < P; ++e) t[e] = both(0.0f);
@@ -556,7 +566,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
     float k1 = 0.0f, k2 = 0.0f;
     if (next) {
       if (STAGED) cols.load_smem(u, ring.read + pitch), cols.load_smem(v, ring.read);
-      else cols.load(u, out + at), cols.load(v, dh + at);
+      else cols.load(u, in(p.out, at)), cols.load(v, in(p.dh, at));
       float2 s1 = both(0.0f);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
     }
     auto load_y = [&]() {
       if (STAGED) cols.load_smem(v, ring.read + s_y);
-      else cols.load(v, y + at);
+      else cols.load(v, in(p.y, at));
     };
     if (has_y) load_y();
     if (next || post) {
@@ -588,7 +598,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
       }
       float a2 = s2.x + s2.y, a3 = s3.x + s3.y;
       // two buffers: a warp may still read row r's while row r + 1 is written
-      block_sum3(k1, a2, a3, red[r & 1], warps);
+      worker_sum3(k1, a2, a3, red[r & 1] + group * warps, warps);
       k1 *= rn * inv_d;                            // r2 mean(q u)
       k2 = rp * rp * rp * (a2 - k1 * a3) * inv_d;  // r1^2 mean(D c); 0 without the norm
       if (has_y && !KEEP_Y) load_y();
@@ -598,14 +608,14 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
       t[e] = fma2(u[e], both(-k1), t[e]);  // D
       u[e] = mul2(t[e], both(p.a));
     }
-    cols.store(dx + at, u);
+    cols.store(to(p.dx, at), u);
     if (has_y) {
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         A[e] = fma2(t[e], mul2(v[e], both(rp)), A[e]);
         u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(v[e], both(-k2)));
       }
-      cols.store(dy + at, u);
+      cols.store(to(p.dy, at), u);
       if (left == 0 || r + 1 == r1) {
         // the gate row, or the worker's range, ends
         float2 g[P], wp[P];
@@ -614,16 +624,17 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
           A[e] = mul2(A[e], both(p.b));
           g[e] = both(1.0f);
         }
-        if (gate) {
-          gate_row(g);
-          gate += p.gate_tokens ? p.gate_stride : 0;
+        if (p.gate) {
+          gate_row(g, r);
           post_weights(wp);
 #pragma unroll
           for (int e = 0; e < P; ++e) wp[e] = mul2(wp[e], A[e]);
           const int gi = p.gate_tokens ? r / p.gate_tokens : 0;
           const long long first = (long long)gi * p.gate_tokens;
           const long long last = p.gate_tokens ? min(first + p.gate_tokens, (long long)p.n) : p.n;
-          if (first < r0)
+          if (gate_all)
+            cols.store_f32(end_gate, wp);
+          else if (first < r0)
             cols.store_f32(p.part_head + (size_t)w * p.pitch, wp);
           else if (last > r1)
             cols.store_f32(p.part_tail + (size_t)w * p.pitch, wp);
@@ -642,18 +653,35 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_bwd_kernel(const NormBwd p) {
     }
     ring.done();
   }
-  const bool alone = p.workers == 1;
-  if (p.w_post) {
-    cols.load_f32(A, sum_post);
-    cols.store_f32(alone ? p.dw_post : p.part_post + (size_t)w * p.pitch, A);
+  if (next) cols.store_f32(end_next, acc_n);
+  if (gate_all && r0 == r1) cols.store_f32(end_gate, A);
+  __syncthreads();
+  // the workers' sums, in their order
+  const bool alone = p.blocks == 1;
+  const size_t ring_f = p.ring_bytes / 4;
+  const float* ends = reinterpret_cast<const float*>(nsm);
+  const float* posts = reinterpret_cast<const float*>(nsm + (size_t)groups * p.ring_bytes);
+  const size_t row = alone ? 0 : (size_t)blockIdx.x * p.pitch;
+  for (int c = group * blockDim.x + threadIdx.x; c < p.d; c += groups * blockDim.x) {
+    float a = 0.0f, b = 0.0f, g = 0.0f;
+    for (int k = 0; k < groups; ++k) {
+      if (post) a += posts[(size_t)k * fpitch + c];
+      if (next) b += ends[k * ring_f + c];
+      if (gate_all) g += ends[k * ring_f + (next ? fpitch : 0) + c];
+    }
+    if (post) (alone ? p.dw_post : p.part_post + row)[c] = a;
+    if (next) (alone ? p.dw_next : p.part_next + row)[c] = b;
+    if (gate_all) {
+      if (alone) static_cast<T*>(p.dgate)[c] = (T)g;
+      else p.part_gate[row + c] = g;
+    }
   }
-  if (p.w_next) cols.store_f32(alone ? p.dw_next : p.part_next + (size_t)w * p.pitch, acc_n);
 }
 
-// Joins the workers' partial sums in worker order: 128 columns a block, 32
-// slices of the workers, then the slices in order. blockIdx.y: dw_post,
-// dw_next, then the gate groups that more than one worker holds, found by
-// group (fewer groups than workers) or by the worker that they begin in.
+// Joins the partial sums in order: 128 columns a block, 32 slices of the
+// partial rows, then the slices. blockIdx.y: dw_post, dw_next, then the gate: its
+// one row, or the rows that more than one worker holds, found by row (fewer
+// rows than workers) or by the worker that they begin in.
 struct NormReduce {
   NormBwd b;
   int by_group;
@@ -666,30 +694,28 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
   pdl_wait();
   const NormBwd& p = q.b;
   const int job = blockIdx.y;
-  const float* first_src;  // worker w_lo's partial row
+  const float* first_src;  // partial row w_lo
   const float* src;        // the others': src + w * pitch
-  int w_lo = 0, w_hi = p.workers;  // workers w_lo .. w_hi - 1
+  int w_lo = 0, w_hi = p.blocks;  // partial rows w_lo .. w_hi - 1
   long long group = 0;
   if (job == 0) {
     if (!p.w_post) return;
-    src = p.part_post;
-    first_src = src;
+    first_src = src = p.part_post;
   } else if (job == 1) {
     if (!p.w_next) return;
-    src = p.part_next;
-    first_src = src;
+    first_src = src = p.part_next;
+  } else if (p.gate_tokens == 0) {
+    first_src = src = p.part_gate;
   } else {
-    const int T0 = p.gate_tokens;
-    long long first, last;
+    const long long tokens = p.gate_tokens;
     if (q.by_group) {
       group = job - 2;
     } else {
       const int end = worker_row(job - 2 + 1, p.n, p.workers);
       if (end == worker_row(job - 2, p.n, p.workers)) return;
-      group = (end - 1) / T0;  // (T0 > 0 here)
+      group = (end - 1) / tokens;
     }
-    first = group * T0;
-    last = T0 ? min(first + T0, (long long)p.n) : p.n;
+    const long long first = group * tokens, last = min(first + tokens, (long long)p.n);
     w_lo = row_worker((int)first, p.n, p.workers);
     w_hi = row_worker((int)last - 1, p.n, p.workers) + 1;
     if (!q.by_group && w_lo != job - 2) return;  // it began earlier
@@ -730,55 +756,68 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
 }
 
 // ---- work split of the backward ---------------------------------------------
-// At least two rows a worker: fewer would only add partial sums to join.
-// Workers an SM: what its registers hold (80 a thread up to 256 threads, 64
-// above).
+// At least two rows a worker: fewer would only add partial sums to join. One
+// block an SM with as many workers as its registers hold (80 a thread up to 256
+// threads a worker, 64 above), fewer where there are not two rows for each.
 constexpr int kBwdMinRows = 2;
-int bwd_workers_per_sm(int d) {
+int bwd_groups(int d) {
   const int t = norm_threads(d);
   const int k = (t <= 256 ? 768 : 1024) / t;
-  return k < 1 ? 1 : k > 16 ? 16 : k;
+  return k < 1 ? 1 : k > 12 ? 12 : k;
 }
-int bwd_workers(int n, int d) {
-  const long long most = (long long)kBlockSms * bwd_workers_per_sm(d);
-  const long long want = (n + kBwdMinRows - 1) / kBwdMinRows;
-  return (int)(want < most ? want : most);
+struct BwdSplit {
+  int workers, groups, blocks;
+};
+BwdSplit bwd_split(int n, int d) {
+  const long long most = (long long)kBlockSms * bwd_groups(d);
+  const long long want = ((long long)n + kBwdMinRows - 1) / kBwdMinRows;
+  BwdSplit s;
+  s.workers = (int)(want < most ? want : most);
+  s.groups = (s.workers + kBlockSms - 1) / kBlockSms;
+  if (s.groups < 1) s.groups = 1;
+  s.blocks = (s.workers + s.groups - 1) / s.groups;
+  return s;
 }
 int bwd_pitch(int d) { return (d + 31) / 32 * 32; }
 
-template <typename T, int VEC, int EPT, bool STAGED, int MAXT, int MINB>
-cudaError_t run_bwd(const NormBwd& p, size_t smem, cudaStream_t s) {
-  auto kern = norm_bwd_kernel<T, VEC, EPT, STAGED, MAXT, MINB>;
-  if (smem > 48 * 1024) {
+template <typename T, int VEC, int EPT, bool STAGED, int MAXT, bool ALL = false>
+cudaError_t run_bwd(const NormBwd& p, int groups, size_t smem, cudaStream_t s) {
+  if constexpr (STAGED && !ALL)
+    if (p.y && p.w_post && p.dh && p.dout)
+      return run_bwd<T, VEC, EPT, STAGED, MAXT, true>(p, groups, smem, s);
+  auto kern = norm_bwd_kernel<T, VEC, EPT, STAGED, MAXT, ALL>;
+  if (smem > 32 * 1024) {  // (48 KB with the static part need no leave)
     const cudaError_t e =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kern, dim3(p.workers), dim3(norm_threads(p.d)), smem, s, p);
+  return launch_pdl(kern, dim3(p.blocks), dim3(norm_threads(p.d), groups), smem, s, p);
 }
 
 template <typename T, int VEC>
-cudaError_t launch_bwd(NormBwd& p, bool vec, cudaStream_t s) {
-  const int per_sm = bwd_workers_per_sm(p.d);
-  const size_t row = (size_t)norm_threads(p.d) * (p.d > 8192 ? 16 : 8) * sizeof(T);
-  const size_t sums = p.w_post ? (size_t)p.d * 4 : 0;
+cudaError_t launch_bwd(NormBwd& p, int groups, bool vec, cudaStream_t s) {
+  const size_t cols = (size_t)norm_threads(p.d) * (p.d > 8192 ? 16 : 8);
+  const size_t row = cols * sizeof(T);
+  const size_t sums = p.w_post ? cols * 4 : 0;
+  const size_t ends = cols * 4 * ((p.w_next ? 1 : 0) + (p.gate && p.gate_tokens == 0 ? 1 : 0));
   p.slots = (p.dh ? 2 : 0) + (p.y ? 1 : 0) + (p.dout ? 1 : 0) +
             (p.gate && p.gate_tokens == 1 ? 1 : 0);
-  const size_t budget = ring_budget(per_sm);
+  const size_t budget = ring_budget(groups);
   const size_t fit = budget > sums ? (budget - sums) / (p.slots * row) : 0;
   const int deep = (p.n + p.workers - 1) / p.workers;
   p.stages = fit > kMaxStages ? kMaxStages : (int)fit;
   if (p.stages > deep) p.stages = deep;
-  if (!vec || p.stages < 1) {
-    p.stages = 1;
-    return p.d > 8192 ? run_bwd<T, 1, 16, false, 1024, 1>(p, sums, s)
-                      : run_bwd<T, 1, 8, false, 1024, 1>(p, sums, s);
-  }
-  const size_t smem = p.stages * p.slots * row + sums;
-  if (p.d > 8192) return run_bwd<T, VEC, 16, true, 1024, 1>(p, smem, s);
-  const int threads = norm_threads(p.d);
-  if (threads <= 256) return run_bwd<T, VEC, 8, true, 256, 3>(p, smem, s);
-  return run_bwd<T, VEC, 8, true, 1024, 1>(p, smem, s);
+  const bool staged = vec && p.stages >= 1 && ends + sums <= budget;
+  if (!staged) p.stages = 1;
+  const size_t ring = staged ? p.stages * p.slots * row : 0;
+  p.ring_bytes = (uint32_t)(ring > ends ? ring : ends);
+  const size_t smem = groups * (p.ring_bytes + sums);
+  if (!staged)
+    return p.d > 8192 ? run_bwd<T, 1, 16, false, 1024>(p, groups, smem, s)
+                      : run_bwd<T, 1, 8, false, 1024>(p, groups, smem, s);
+  if (p.d > 8192) return run_bwd<T, VEC, 16, true, 1024>(p, groups, smem, s);
+  if (norm_threads(p.d) <= 256) return run_bwd<T, VEC, 8, true, 768>(p, groups, smem, s);
+  return run_bwd<T, VEC, 8, true, 1024>(p, groups, smem, s);
 }
 
 moe_status norm_check(const moe_norm_config* c) {
@@ -835,8 +874,13 @@ moe_status forward_impl(const moe_norm_config* c, const NormFwd& q, cudaStream_t
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
+// Partial rows: dw_post, dw_next and the one gate row a block, or two of the
+// gate rows a worker.
 size_t backward_bytes(const moe_norm_config* c) {
-  const size_t b = (size_t)4 * bwd_workers(c->n, c->d) * bwd_pitch(c->d) * sizeof(float);
+  const BwdSplit k = bwd_split(c->n, c->d);
+  const size_t rows =
+      c->gate_tokens ? 2 * (size_t)k.blocks + 2 * (size_t)k.workers : 3 * (size_t)k.blocks;
+  const size_t b = rows * bwd_pitch(c->d) * sizeof(float);
   return b < 256 ? 256 : b;
 }
 
@@ -873,26 +917,31 @@ moe_status backward_impl(const moe_norm_config* c, const NormBwd& q, void* ws, s
   if (!element_aligned(c, {p.dout, p.dh, p.out, p.y, p.gate, p.dx, p.dy, p.dgate}) ||
       !f32_aligned({p.w_post, p.w_next, p.rstd_post, p.rstd_next, p.dw_post, p.dw_next}))
     return MOE_ERR_INVALID_ARG;
-  p.workers = bwd_workers(c->n, c->d);
+  const BwdSplit k = bwd_split(c->n, c->d);
+  p.workers = k.workers;
+  p.blocks = k.blocks;
   p.pitch = bwd_pitch(c->d);
-  const size_t each = (size_t)p.workers * p.pitch;
   p.part_post = static_cast<float*>(ws);
-  p.part_next = p.part_post + each;
-  p.part_head = p.part_next + each;
-  p.part_tail = p.part_head + each;
+  p.part_next = p.part_post + (size_t)k.blocks * p.pitch;
+  p.part_gate = p.part_head = p.part_next + (size_t)k.blocks * p.pitch;
+  p.part_tail = p.part_head + (size_t)k.workers * p.pitch;
   const bool vec = vectors(c, p.gate != nullptr,
                            {p.dout, p.dh, p.out, p.y, p.gate, p.dx, p.dy, p.dgate, p.w_post,
-                            p.w_next, p.dw_post, p.dw_next});
-  cudaError_t e = c->dtype == MOE_BF16 ? launch_bwd<__nv_bfloat16, 8>(p, vec, s)
-                                       : launch_bwd<float, 4>(p, vec, s);
+                            p.w_next});
+  cudaError_t e = c->dtype == MOE_BF16 ? launch_bwd<__nv_bfloat16, 8>(p, k.groups, vec, s)
+                                       : launch_bwd<float, 4>(p, k.groups, vec, s);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
-  if (p.workers == 1) return MOE_OK;
+  const bool shared_rows = p.gate && p.gate_tokens > 1;  // gate rows of several workers
+  if (p.blocks == 1 && (!shared_rows || p.workers == 1)) return MOE_OK;
   NormReduce r{p, 0};
+  if (p.blocks == 1) r.b.w_post = r.b.w_next = nullptr;  // (written already)
   int jobs = 2;
-  if (p.gate && p.gate_tokens != 1) {
-    const int groups = gate_rows(c);
-    r.by_group = groups <= p.workers;
-    jobs += r.by_group ? groups : p.workers;
+  if (shared_rows) {
+    const int rows = gate_rows(c);
+    r.by_group = rows <= p.workers;
+    jobs += r.by_group ? rows : p.workers;
+  } else if (p.gate && p.gate_tokens == 0) {
+    ++jobs;
   }
   const dim3 grid((p.pitch + 127) / 128, jobs), block(32, kRedSlices);
   e = c->dtype == MOE_BF16 ? launch_pdl(norm_reduce_kernel<__nv_bfloat16>, grid, block, 0, s, r)
