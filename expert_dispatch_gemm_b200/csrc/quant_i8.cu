@@ -4,12 +4,21 @@
 //   s = max_j |x_j| / 127 (fp32)      q_j = x_j / s, to nearest, ties to even
 //
 // The rounding is decided on the exact quotient, so q is a function of x
-// alone and not of how a reciprocal rounds: t = rint(x (1/s)) is at most one
-// step off, the remainder x - t s is exact in one fma (t s and x agree to a
-// step, so their difference fits 24 bits), and comparing its double with s
-// says whether the neighbour is nearer. Few elements come that close to a
-// border; the others pay one fma and one compare. Bound by HBM: it reads each
-// element once and writes one byte for it.
+// alone and not of how a reciprocal rounds. t = x c + 1.5 2^23 in one fma
+// rounds to an integer, with c within a few steps (2^-24 each) of 1 / s; that
+// is x / s rounded unless x / s lies that close to a border m / 2, m odd.
+// - fp32: the remainder x - t s is exact in one fma (t s and x agree to a step,
+//   so their difference fits 24 bits); where its double reaches s the element
+//   is rounded again with care.
+// - bf16: with integer significands below 2^8, x = X 2^i, max = M 2^(i+k), and
+//   Q = 127 x / max = 127 X / (M 2^k) is m / 2 or at least 1 / (2 M 2^k) >=
+//   2^-9 2^-k away from it, where all the errors (of c, and of s against
+//   max / 127) come to less than 2^-15 2^-k. Only where Q is m / 2 itself does the
+//   side count, and there x / s lies below m / 2 if s was rounded up, above if
+//   down: c is taken strictly below or above 127 / max accordingly (and is
+//   exact where s is), and no element needs a check.
+// Bound by HBM: it reads each element once and writes one byte for it, about
+// 10 elements a clock an SM, of which the checks would have taken half.
 //
 // "Expert choice routing" (aicassindra.com), "The math": X_in[e] = P[e] X. A
 // permutation of rows commutes with a scale per row, so the dispatch gathers
@@ -23,7 +32,13 @@
 namespace moe {
 namespace {
 
-// ---- VEC consecutive elements: 16 bytes read, VEC bytes written ------------
+// ---- VEC consecutive elements: 16 bytes read (VEC > 1), VEC bytes written ----
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <typename T, int VEC>
 struct QChunk;
 template <>
@@ -37,6 +52,13 @@ struct QChunk<__nv_bfloat16, 8> {
     const uint32_t w = i < 2 ? r.x : i < 4 ? r.y : i < 6 ? r.z : r.w;
     return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
   }
+  // the largest magnitude; NaN where there is one
+  __device__ __forceinline__ float most() const {
+    auto h = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+    const __nv_bfloat162 m =
+        __hmax2_nan(__hmax2_nan(h(r.x), h(r.y)), __hmax2_nan(h(r.z), h(r.w)));
+    return max_nan(__low2float(m), __high2float(m));
+  }
 };
 template <>
 struct QChunk<float, 4> {
@@ -48,6 +70,9 @@ struct QChunk<float, 4> {
   __device__ __forceinline__ float get(int i) const {
     return i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
   }
+  __device__ __forceinline__ float most() const {
+    return max_nan(max_nan(fabsf(r.x), fabsf(r.y)), max_nan(fabsf(r.z), fabsf(r.w)));
+  }
 };
 template <>
 struct QChunk<__nv_bfloat16, 1> {
@@ -57,6 +82,7 @@ struct QChunk<__nv_bfloat16, 1> {
   }
   __device__ __forceinline__ void zero() { r = 0; }
   __device__ __forceinline__ float get(int) const { return bf16_to_f32(r); }
+  __device__ __forceinline__ float most() const { return fabsf(get(0)); }
 };
 template <>
 struct QChunk<float, 1> {
@@ -64,31 +90,46 @@ struct QChunk<float, 1> {
   __device__ __forceinline__ void load(const float* p) { r = *p; }
   __device__ __forceinline__ void zero() { r = 0.0f; }
   __device__ __forceinline__ float get(int) const { return r; }
+  __device__ __forceinline__ float most() const { return fabsf(r); }
 };
 
-// The largest magnitude, with every NaN above every number: magnitudes
-// compare as their bit patterns.
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Magnitudes, a NaN above all, compare as their bit patterns.
+__device__ __forceinline__ uint32_t warp_most(float v) {
+  return __reduce_max_sync(~0u, __float_as_uint(v) & 0x7fffffffu);
+}
 
+enum { ROW_PLAIN, ROW_DEAD, ROW_TINY };
 struct RowScale {
-  float s, inv;
-  bool plain;  // inv is a normal number: x * inv is within two roundings of x / s
-  bool dead;   // a row of zeros, or one that is not finite: all q are 0
+  float s, c;
+  // DEAD: a row of zeros, or one that is not finite: all q are 0.
+  // TINY: 1 / s may not be a normal number, the quotient is taken by division
+  int kind;
 };
 
+template <typename T>
 __device__ __forceinline__ RowScale row_scale(uint32_t most) {
   RowScale r;
-  const float a = __uint_as_float(most);
-  r.dead = most == 0 || most >= 0x7f800000u;
-  r.s = most >= 0x7f800000u ? __uint_as_float(0x7fffffffu) : __fdiv_rn(a, 127.0f);
-  if (!r.dead && r.s == 0.0f) r.dead = true;  // below the smallest fp32 step
-  r.plain = r.s >= 0x1p-100f;
-  r.inv = r.plain ? 1.0f / r.s : 0.0f;
+  const bool finite = most < 0x7f800000u;
+  const float max = __uint_as_float(most);
+  r.s = finite ? __fdiv_rn(max, 127.0f) : __uint_as_float(0x7fffffffu);
+  r.kind = !finite || r.s == 0.0f ? ROW_DEAD : r.s < 0x1p-100f ? ROW_TINY : ROW_PLAIN;
+  r.c = 0.0f;
+  if (r.kind == ROW_PLAIN) {
+    if (sizeof(T) == 2) {
+      const float over = __fmaf_rn(127.0f, r.s, -max);  // exact: s was rounded up or down
+      const float c = __fdiv_rn(127.0f, max);           // two steps off it is past 127 / max
+      r.c = over == 0.0f ? c : __int_as_float(__float_as_int(c) + (over > 0.0f ? -2 : 2));
+    } else {
+      r.c = __fdiv_rn(1.0f, r.s);
+    }
+  }
   return r;
 }
 
-// round(x / s) given a candidate t at most one off
-__device__ __noinline__ float fix_round(float x, float t, float s) {
+constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
+
+// x / s to the nearest integer, ties to even, from a candidate t at most one off
+__device__ __forceinline__ float fix_round(float x, float t, float s) {
   const float r2 = 2.0f * fmaf(-t, s, x);
   const float odd = t - 2.0f * floorf(t * 0.5f);
   if (r2 > s || (r2 == s && odd != 0.0f)) t += 1.0f;
@@ -96,40 +137,61 @@ __device__ __noinline__ float fix_round(float x, float t, float s) {
   return t;
 }
 
-constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer
-
+// The rows that the fast path leaves: dead ones, and those of a tiny scale (a
+// few steps coarse as a denormal, so that the quotient may pass 127).
 template <typename T, int VEC>
-__device__ __forceinline__ void quantize(const QChunk<T, VEC>& c, const RowScale& k, int* q) {
-  float t[VEC];
-  bool near = false;
-#pragma unroll
+__device__ __noinline__ uint64_t quantize_slow(const QChunk<T, VEC> c, float s, int kind) {
+  uint64_t out = 0;
+  if (kind == ROW_DEAD) return 0;
   for (int j = 0; j < VEC; ++j) {
     const float x = c.get(j);
-    t[j] = k.plain ? __fadd_rn(__fadd_rn(x * k.inv, kMagic), -kMagic)
-                   : rintf(__fdiv_rn(x, k.s));
-    near |= fabsf(2.0f * fmaf(-t[j], k.s, x)) >= k.s;
+    const float t = fix_round(x, rintf(__fdiv_rn(x, s)), s);
+    out |= (uint64_t)(uint8_t)(int8_t)(int)fminf(fmaxf(t, -127.0f), 127.0f) << (8 * j);
   }
-  if (near) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) t[j] = fix_round(c.get(j), t[j], k.s);
-  }
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    // (a denormal scale is a few steps coarse: the quotient may pass 127)
-    const float v = fminf(fmaxf(t[j], -127.0f), 127.0f);
-    q[j] = k.dead ? 0 : (__float_as_int(__fadd_rn(v, kMagic)) & 0xff);
-  }
+  return out;
 }
 
-template <int VEC>
-__device__ __forceinline__ uint64_t pack_bytes(const int* q) {
-  uint32_t lo = 0, hi = 0;
+// VEC bytes: the low bytes of x c + kMagic (|t| <= 127, as |x| <= 127 s (1 + 2^-24)).
+template <typename T, int VEC>
+__device__ __forceinline__ uint64_t quantize(const QChunk<T, VEC>& c, const RowScale& k) {
+  if (k.kind != ROW_PLAIN) return quantize_slow<T, VEC>(c, k.s, k.kind);
+  uint32_t b[VEC];
+  float far = 0.0f;
+  if constexpr (VEC == 1) {
+    const float v = __fmaf_rn(c.get(0), k.c, kMagic);
+    b[0] = __float_as_uint(v);
+    if (sizeof(T) == 4) far = fabsf(__fmaf_rn(kMagic - v, k.s, c.get(0)));
+  } else {
+    const float2 cc = make_float2(k.c, k.c), s = make_float2(k.s, k.s);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    if (j < 4) lo |= (uint32_t)q[j] << (8 * j);
-    else hi |= (uint32_t)q[j] << (8 * (j - 4));
+    for (int j = 0; j < VEC; j += 2) {
+      const float2 x = make_float2(c.get(j), c.get(j + 1));
+      const float2 v = __ffma2_rn(x, cc, make_float2(kMagic, kMagic));
+      b[j] = __float_as_uint(v.x);
+      b[j + 1] = __float_as_uint(v.y);
+      if constexpr (sizeof(T) == 4) {
+        // (kMagic - v is exact)
+        const float2 r = __ffma2_rn(
+            __ffma2_rn(v, make_float2(-1.0f, -1.0f), make_float2(kMagic, kMagic)), s, x);
+        far = fmaxf(far, fmaxf(fabsf(r.x), fabsf(r.y)));
+      }
+    }
   }
-  return (uint64_t)hi << 32 | lo;
+  if (sizeof(T) == 4 && 2.0f * far >= k.s) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      b[j] = __float_as_uint(fix_round(c.get(j), __uint_as_float(b[j]) - kMagic, k.s) + kMagic);
+  }
+  if constexpr (VEC == 1) {
+    return b[0] & 0xff;
+  } else {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4)
+      w[j / 4] = __byte_perm(__byte_perm(b[j], b[j + 1], 0x0040),
+                             __byte_perm(b[j + 2], b[j + 3], 0x0040), 0x5410);
+    return (uint64_t)w[1] << 32 | w[0];
+  }
 }
 
 template <int VEC>
@@ -138,8 +200,6 @@ __device__ __forceinline__ void store_bytes(int8_t* p, uint64_t v) {
   else if constexpr (VEC == 4) *reinterpret_cast<uint32_t*>(p) = (uint32_t)v;
   else *p = (int8_t)v;
 }
-
-__device__ __forceinline__ uint32_t warp_max(uint32_t v) { return __reduce_max_sync(~0u, v); }
 
 // ---------------------------------------------------------------------------
 // quantise rows
@@ -156,10 +216,10 @@ struct QuantArgs {
 
 constexpr int kQWarps = 8;
 
-// Rows of the groups, in order, dealt out to row owners (a warp, or with
-// BLOCK the whole block) in a grid-wide stride; each keeps its row in
-// registers between the maximum and the rounding. ITEMS == 0: a row longer
-// than the registers of a block is read twice.
+// The rows of the groups, in order, in one contiguous run for each row owner
+// (a warp, or with BLOCK the whole block). A row stays in registers between
+// the maximum and the rounding, and the next one is loaded meanwhile. ITEMS ==
+// 0: a row longer than the registers of a block is read twice.
 template <typename T, int VEC, int ITEMS, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kQWarps) quantize_kernel(const QuantArgs a) {
   __shared__ int start[MOE_I8_MAX_GROUPS];
@@ -199,63 +259,80 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kQWarps) quantize_kernel(c
   const int tid = BLOCK ? threadIdx.x : lane;
   const int threads = BLOCK ? blockDim.x : 32;
   const int chunks = a.cols / VEC;
-  int flip = 0;
-  for (long long i = owner; i < total; i += owners) {
-    long long row = i;
-    if (a.starts) {
-      int lo = 0, hi = a.groups - 1;
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= i) lo = mid; else hi = mid - 1;
-      }
-      row = start[lo] + (i - prefix[lo]);
+  const long long first = total * owner / owners, last = total * (owner + 1) / owners;
+  if (first >= last) return;
+  // the row being loaded, and the rows left after it in its group
+  int g = 0;
+  long long row = first, left = last - first - 1;
+  if (a.starts) {
+    int hi = a.groups - 1;
+    while (g < hi) {
+      const int mid = (g + hi + 1) >> 1;
+      if (prefix[mid] <= first) g = mid; else hi = mid - 1;
     }
-    const T* x = static_cast<const T*>(a.x) + (size_t)row * a.cols;
-    int8_t* q = a.q + (size_t)row * a.cols;
+    row = start[g] + (first - prefix[g]);
+    left = prefix[g + 1] - first - 1;
+  }
+  QChunk<T, VEC> ahead[ITEMS > 0 ? ITEMS : 1];
+  const T* x = static_cast<const T*>(a.x) + (size_t)row * a.cols + (size_t)tid * VEC;
+  auto fetch = [&]() {
+#pragma unroll
+    for (int k = 0; k < ITEMS; ++k) {
+      ahead[k].zero();
+      if (k * threads + tid < chunks) ahead[k].load(x + (size_t)k * threads * VEC);
+    }
+  };
+  fetch();
+  for (int i = (int)(last - first); i > 0; --i) {
+    int8_t* q = a.q + (size_t)row * a.cols + (size_t)tid * VEC;
+    float* scale = a.scale + row;
     QChunk<T, VEC> c[ITEMS > 0 ? ITEMS : 1];
-    uint32_t most = 0;
+    float m = 0.0f;
     if constexpr (ITEMS > 0) {
 #pragma unroll
-      for (int k = 0; k < ITEMS; ++k) {
-        const int p = k * threads + tid;
-        c[k].zero();
-        if (p < chunks) c[k].load(x + (size_t)p * VEC);
-      }
-#pragma unroll
-      for (int k = 0; k < ITEMS; ++k)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) most = max(most, magnitude(c[k].get(j)));
+      for (int k = 0; k < ITEMS; ++k) c[k] = ahead[k];
     } else {
       for (int p = tid; p < chunks; p += threads) {
-        c[0].load(x + (size_t)p * VEC);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) most = max(most, magnitude(c[0].get(j)));
+        c[0].load(x + (size_t)(p - tid) * VEC);
+        m = max_nan(m, c[0].most());
       }
     }
-    most = warp_max(most);
+    const T* now = x;
+    if (i > 1) {
+      if (left > 0) {
+        --left;
+        ++row;
+        x += a.cols;
+      } else {  // the next group that has a row
+        do ++g;
+        while (prefix[g + 1] == prefix[g]);
+        row = start[g];
+        left = prefix[g + 1] - prefix[g] - 1;
+        x = static_cast<const T*>(a.x) + (size_t)row * a.cols + (size_t)tid * VEC;
+      }
+      fetch();
+    }
+    if constexpr (ITEMS > 0) {
+#pragma unroll
+      for (int k = 0; k < ITEMS; ++k) m = max_nan(m, c[k].most());
+    }
+    uint32_t most = warp_most(m);
     if (BLOCK) {
-      if (lane == 0) red[flip][threadIdx.x >> 5] = most;
+      if (lane == 0) red[i & 1][threadIdx.x >> 5] = most;
       __syncthreads();
-      most = warp_max(lane < (int)(blockDim.x >> 5) ? red[flip][lane] : 0u);
-      flip ^= 1;
+      most = __reduce_max_sync(~0u, lane < (int)(blockDim.x >> 5) ? red[i & 1][lane] : 0u);
     }
-    const RowScale k = row_scale(most);
-    if (tid == 0) a.scale[row] = k.s;
-    int v[VEC];
+    const RowScale k = row_scale<T>(most);
+    if (tid == 0) *scale = k.s;
     if constexpr (ITEMS > 0) {
 #pragma unroll
-      for (int m = 0; m < ITEMS; ++m) {
-        const int p = m * threads + tid;
-        if (p < chunks) {
-          quantize<T, VEC>(c[m], k, v);
-          store_bytes<VEC>(q + (size_t)p * VEC, pack_bytes<VEC>(v));
-        }
-      }
+      for (int j = 0; j < ITEMS; ++j)
+        if (j * threads + tid < chunks)
+          store_bytes<VEC>(q + (size_t)j * threads * VEC, quantize<T, VEC>(c[j], k));
     } else {
       for (int p = tid; p < chunks; p += threads) {
-        c[0].load(x + (size_t)p * VEC);
-        quantize<T, VEC>(c[0], k, v);
-        store_bytes<VEC>(q + (size_t)p * VEC, pack_bytes<VEC>(v));
+        c[0].load(now + (size_t)(p - tid) * VEC);
+        store_bytes<VEC>(q + (size_t)(p - tid) * VEC, quantize<T, VEC>(c[0], k));
       }
     }
   }
@@ -263,26 +340,24 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kQWarps) quantize_kernel(c
 
 template <typename T, int VEC, int ITEMS, bool BLOCK>
 cudaError_t run_quant(const QuantArgs& a, int threads, cudaStream_t s) {
-  // resident blocks: up to 2,048 threads an SM, the rows dealt out in a stride
+  // resident blocks: 1,024 threads an SM, in up to 16 blocks
   const long long per_block = BLOCK ? 1 : kQWarps;
-  const int resident = BLOCK ? (2048 / threads < 8 ? 2048 / threads : 8) : 8;
+  const int resident = 1024 / threads > 16 ? 16 : 1024 / threads;
   long long grid = (a.rows + per_block - 1) / per_block;
   if (grid > (long long)kBlockSms * resident) grid = (long long)kBlockSms * resident;
   return launch_pdl(quantize_kernel<T, VEC, ITEMS, BLOCK>, dim3((unsigned)grid), dim3(threads), 0,
                     s, a);
 }
 
-// A warp a row while a lane holds at most 32 bf16 (16 fp32) elements, then a
-// block a row with up to 4 vectors a thread.
+// A warp a row while a lane holds at most 4 vectors, then a block a row with
+// up to 4 vectors a thread.
 template <typename T, int VEC>
 cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s) {
   const int chunks = a.cols / VEC;
-  constexpr int I4 = 4;
-  if (chunks <= 32 * I4) return run_quant<T, VEC, I4, false>(a, 32 * kQWarps, s);
-  if (chunks <= 1024 * I4) {
-    const int threads = ((chunks + I4 - 1) / I4 + 31) / 32 * 32;
-    return run_quant<T, VEC, I4, true>(a, threads, s);
-  }
+  if (chunks <= 32) return run_quant<T, VEC, 1, false>(a, 32 * kQWarps, s);
+  if (chunks <= 32 * 4) return run_quant<T, VEC, 4, false>(a, 32 * kQWarps, s);
+  if (chunks <= 1024 * 4)
+    return run_quant<T, VEC, 4, true>(a, ((chunks + 3) / 4 + 31) / 32 * 32, s);
   return run_quant<T, VEC, 0, true>(a, 1024, s);
 }
 
@@ -325,7 +400,7 @@ __global__ void __launch_bounds__(1024) dispatch_i8_kernel(const DispatchI8 a) {
   const T* x = static_cast<const T*>(a.X) + (size_t)t * a.d;
   const int chunks = a.d / VEC;
   QChunk<T, VEC> c[ITEMS > 0 ? ITEMS : 1];
-  uint32_t most = 0;
+  float m = 0.0f;
   if constexpr (ITEMS > 0) {
 #pragma unroll
     for (int k = 0; k < ITEMS; ++k) {
@@ -334,42 +409,34 @@ __global__ void __launch_bounds__(1024) dispatch_i8_kernel(const DispatchI8 a) {
       if (p < chunks) c[k].load(x + (size_t)p * VEC);
     }
 #pragma unroll
-    for (int k = 0; k < ITEMS; ++k)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) most = max(most, magnitude(c[k].get(j)));
+    for (int k = 0; k < ITEMS; ++k) m = max_nan(m, c[k].most());
   } else {
     for (int p = tid; p < chunks; p += threads) {
       c[0].load(x + (size_t)p * VEC);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) most = max(most, magnitude(c[0].get(j)));
+      m = max_nan(m, c[0].most());
     }
   }
-  most = warp_max(most);
+  uint32_t most = warp_most(m);
   if (lane == 0) red[tid >> 5] = most;
   __syncthreads();
-  most = warp_max(lane < threads / 32 ? red[lane] : 0u);
-  const RowScale k = row_scale(most);
+  most = __reduce_max_sync(~0u, lane < threads / 32 ? red[lane] : 0u);
+  const RowScale k = row_scale<T>(most);
   for (int j = tid; j < targets; j += threads)
     if (dst[j] >= 0) a.scale[dst[j]] = k.s;
-  int v[VEC];
   auto put = [&](int p, uint64_t bytes) {
     for (int j = 0; j < targets; ++j)
       if (dst[j] >= 0) store_bytes<VEC>(a.q + (size_t)dst[j] * a.d + (size_t)p * VEC, bytes);
   };
   if constexpr (ITEMS > 0) {
 #pragma unroll
-    for (int m = 0; m < ITEMS; ++m) {
-      const int p = m * threads + tid;
-      if (p < chunks) {
-        quantize<T, VEC>(c[m], k, v);
-        put(p, pack_bytes<VEC>(v));
-      }
+    for (int j = 0; j < ITEMS; ++j) {
+      const int p = j * threads + tid;
+      if (p < chunks) put(p, quantize<T, VEC>(c[j], k));
     }
   } else {
     for (int p = tid; p < chunks; p += threads) {
       c[0].load(x + (size_t)p * VEC);
-      quantize<T, VEC>(c[0], k, v);
-      put(p, pack_bytes<VEC>(v));
+      put(p, quantize<T, VEC>(c[0], k));
     }
   }
 }
