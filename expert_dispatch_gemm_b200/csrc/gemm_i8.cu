@@ -102,13 +102,16 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, State* st, 
   auto probe = [&]() {
     return CLUSTER ? sm100::mbar_try_wait_cluster(bar, parity) : sm100::mbar_try_wait(bar, parity);
   };
-  if (probe()) return true;
-  const uint64_t t0 = global_timer_ns();
+  // the clock is read from the 64th probe on: reading it takes longer than
+  // most waits have left
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (probe()) return true;
     if ((it & 63u) == 0) {
       if (st->abort_flag) return false;
-      if (global_timer_ns() - t0 > kWaitNs) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitNs) {
         st->abort_flag = 1;
         report_error(err, code);
         return false;
@@ -220,40 +223,79 @@ __device__ __forceinline__ float silu_times(float u, float v) {
   return u * __frcp_rn(1.0f + e) * v;
 }
 
-// Epilogue staging of a warp, [32 rows][32 channels] bf16: the tile leaves as
-// 16-byte stores of each row's 32 channels. fp32 outputs are not staged (the
-// ring leaves no room): the 32 lanes write a row's 128 consecutive bytes.
+// Epilogue of bf16 outputs. A lane of the accumulator is a channel, a row of
+// the output is a column of it, so a tile has to be transposed on its way out.
+// The accumulator is read as MMA fragments (two neighbouring rows of a channel
+// in a thread): they are scaled as pairs, converted as pairs and stored as 8 x
+// 8 blocks, transposed by stmatrix, into the warp's staging buffer, from which
+// each row's 32 channels leave as 16-byte stores. 1/8 of the shared-memory
+// stores and about a third of the instructions that storing one element at a
+// time takes. Rows are 80 bytes apart, so that the eight 16-byte pieces of a
+// block lie in different banks.
+constexpr int kStagePitch = 80;
 struct Staging {
-  __nv_bfloat16 v[32][32];
+  unsigned char v[32 * kStagePitch];  // [32 rows][32 channels] bf16
+  float scale[32];                    // the rows' scales
 };
 
-// 32 rows from column cc of the tile on: value(i, x_scale of row i) for each
-template <typename OUT, class F>
-__device__ __forceinline__ void emit(Staging* stg, const I8Params& p, const Tile& t, int cc,
-                                     int col0, int lane, const F& value) {
+// this lane's place in a stmatrix of one 8-row block
+__device__ __forceinline__ uint32_t block_addr(const Staging* s, int lane) {
+  return sm100::smem_addr(s->v) + (lane & 7) * kStagePitch + (lane >> 3) * 16;
+}
+
+__device__ __forceinline__ float2 scaled(uint32_t a, uint32_t b, float2 s) {
+  return __fmul2_rn(make_float2((float)(int)a, (float)(int)b), s);
+}
+__device__ __forceinline__ float2 pair_scale(float2 xs, float ws) {
+  return __fmul2_rn(xs, make_float2(ws, ws));
+}
+
+// the staged rows [0, 32) to rows cc .. of the tile
+__device__ __forceinline__ void store_staged(const Staging* s, const I8Params& p, const Tile& t,
+                                             int cc, int col0, int lane) {
+  __syncwarp();
+  __nv_bfloat16* out =
+      static_cast<__nv_bfloat16*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int i = k * 8 + (lane >> 2), c = lane & 3;
+    const uint4 v = *reinterpret_cast<const uint4*>(s->v + i * kStagePitch + c * 16);
+    if (cc + i < t.valid && col0 + c * 8 < p.n_out)
+      *reinterpret_cast<uint4*>(out + (size_t)i * p.n_out + c * 8) = v;
+  }
+  __syncwarp();
+}
+
+// the scales of rows cc + [0, 32) of the tile
+__device__ __forceinline__ void stage_scales(Staging* s, const I8Params& p, const Tile& t, int cc,
+                                             int lane) {
+  s->scale[lane] = cc + lane < t.valid ? p.x_scale[t.row + cc + lane] : 0.0f;
+  __syncwarp();
+}
+
+// the scales of a thread's channels lane / 4 + 8 k of the warp's 32 from col0 on
+__device__ __forceinline__ void channel_scales(float (&ws)[4], const float* scale,
+                                               const I8Params& p, const Tile& t, int col0,
+                                               int lane) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int c = col0 + (lane >> 2) + 8 * k;
+    ws[k] = c < p.n_out ? scale[(size_t)t.group * p.n_out + c] : 0.0f;
+  }
+}
+
+// fp32 outputs: a lane keeps its channel, and the warp writes the 128
+// consecutive bytes of a row's 32 channels: value(i, x_scale of row i)
+template <class F>
+__device__ __forceinline__ void emit_f32(const I8Params& p, const Tile& t, int cc, int col0,
+                                         int lane, const F& value) {
   const float mine = cc + lane < t.valid ? p.x_scale[t.row + cc + lane] : 0.0f;
-  OUT* out = static_cast<OUT*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
-  sm100::tmem_ld_wait();
-  if constexpr (sizeof(OUT) == 4) {
-    const bool real = col0 + lane < p.n_out;
+  float* out = static_cast<float*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
+  const bool real = col0 + lane < p.n_out;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float r = value(i, __shfl_sync(~0u, mine, i));
-      if (real && cc + i < t.valid) out[(size_t)i * p.n_out + lane] = r;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      stg->v[i][lane] = __float2bfloat16_rn(value(i, __shfl_sync(~0u, mine, i)));
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int idx = k * 32 + lane, i = idx >> 2, c = (idx & 3) * 8;
-      if (cc + i < t.valid && col0 + c < p.n_out)
-        *reinterpret_cast<uint4*>(out + (size_t)i * p.n_out + c) =
-            *reinterpret_cast<const uint4*>(&stg->v[i][c]);
-    }
-    __syncwarp();
+  for (int i = 0; i < 32; ++i) {
+    const float r = value(i, __shfl_sync(~0u, mine, i));
+    if (real && cc + i < t.valid) out[(size_t)i * p.n_out + lane] = r;
   }
 }
 
@@ -287,6 +329,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     st->abort_flag = 0;
     sm100::fence_mbar_init();
   }
+  if (warp == 0 && lane < kBoxes) sm100::tma_prefetch_desc(&tx.m[lane]);
+  if (warp == 0 && lane == kBoxes) sm100::tma_prefetch_desc(&tw);
   if (warp == 1) {
     sm100::tmem_alloc_pair(&st->tmem_base, kTmemCols);
     sm100::tmem_relinquish_pair();
@@ -379,23 +423,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // epilogue of stream sx: warp q = warp % 4 owns lanes (channels) 32q..32q+31
     // and walks the tile's rows, 32 at a time
     const int q = warp & 3;
+    Staging* stg = staging + (warp - 4);
+    const uint32_t blk = block_addr(stg, lane);
     int local = 0;
     for (int tile = first; tile < total; tile += step, ++local) {
       const Tile t = decode(tile, p, st->g);
       const int col0 = t.m0 + (int)rank * 128 + 32 * q;
-      const float ws =
-          col0 + lane < p.n_out ? p.w_scale[(size_t)t.group * p.n_out + col0 + lane] : 0.0f;
+      float ws[4];
+      if constexpr (sizeof(OUT) == 2) {
+        channel_scales(ws, p.w_scale, p, t, col0, lane);
+      } else {
+        ws[0] = col0 + lane < p.n_out ? p.w_scale[(size_t)t.group * p.n_out + col0 + lane] : 0.0f;
+      }
       if (!wait<true>(&st->tfull[sx], (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x64))
         break;
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(sx * 256);
 #pragma unroll 1
       for (int cc = 0; cc < t.n; cc += 32) {
-        uint32_t v[32];
-        sm100::tmem_ld_32x32b_x32(tbase + cc, v);
-        emit<OUT>(&staging[warp - 4], p, t, cc, col0, lane, [&](int i, float xs) {
-          return activate<ACT>((float)(int)v[i] * (xs * ws));
-        });
+        if constexpr (sizeof(OUT) == 2) {
+          uint32_t lo[16], hi[16];  // lanes 0-15 and 16-31 of the quadrant
+          sm100::tmem_ld_16x256b_x4(tbase + cc, lo);
+          sm100::tmem_ld_16x256b_x4(tbase + (16u << 16) + cc, hi);
+          stage_scales(stg, p, t, cc, lane);
+          sm100::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 xs =
+                *reinterpret_cast<const float2*>(&stg->scale[8 * j + 2 * (lane & 3)]);
+            uint32_t r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t* v = (k < 2 ? lo : hi) + 4 * j + 2 * (k & 1);
+              const float2 u = scaled(v[0], v[1], pair_scale(xs, ws[k]));
+              r[k] = pack_bf16x2(activate<ACT>(u.x), activate<ACT>(u.y));
+            }
+            sm100::stmatrix_x4_trans(blk + j * 8 * kStagePitch, r);
+          }
+          store_staged(stg, p, t, cc, col0, lane);
+        } else {
+          uint32_t v[32];
+          sm100::tmem_ld_32x32b_x32(tbase + cc, v);
+          sm100::tmem_ld_wait();
+          emit_f32(p, t, cc, col0, lane, [&](int i, float xs) {
+            return activate<ACT>((float)(int)v[i] * (xs * ws[0]));
+          });
+        }
       }
       sm100::tc_fence_before();
       sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty[sx]), 0));
@@ -440,6 +513,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     st->abort_flag = 0;
     sm100::fence_mbar_init();
   }
+  if (warp == 0 && lane < kBoxes) sm100::tma_prefetch_desc(&tx.m[lane]);
+  if (warp == 0 && lane == kBoxes) sm100::tma_prefetch_desc(&tw);
+  if (warp == 0 && lane == kBoxes + 1) sm100::tma_prefetch_desc(&tw3);
   if (warp == 1) {
     sm100::tmem_alloc_pair(&st->tmem_base, kTmemCols);
     sm100::tmem_relinquish_pair();
@@ -533,24 +609,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // 32-row groups; u in columns [0, 256), v in [256, 512)
     const int q = warp & 3;
     const int half = (warp - 4) >> 2;
+    Staging* stg = staging + (warp - 4);
+    const uint32_t blk = block_addr(stg, lane);
     int local = 0;
     for (int tile = pair_id; tile < total; tile += num_pairs, ++local) {
       const Tile t = decode(tile, p, st->g);
       const int col0 = t.m0 + (int)rank * 128 + 32 * q;
-      const bool real = col0 + lane < p.n_out;  // (a tile may pass the last channel)
-      const size_t wi = (size_t)t.group * p.n_out + col0 + lane;
-      const float ws1 = real ? p.w_scale[wi] : 0.0f, ws3 = real ? p.w3_scale[wi] : 0.0f;
+      float ws1[4], ws3[4];
+      if constexpr (sizeof(OUT) == 2) {
+        channel_scales(ws1, p.w_scale, p, t, col0, lane);
+        channel_scales(ws3, p.w3_scale, p, t, col0, lane);
+      } else {
+        const bool real = col0 + lane < p.n_out;  // (a tile may pass the last channel)
+        const size_t wi = (size_t)t.group * p.n_out + col0 + lane;
+        ws1[0] = real ? p.w_scale[wi] : 0.0f;
+        ws3[0] = real ? p.w3_scale[wi] : 0.0f;
+      }
       if (!wait<true>(&st->tfull, (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x74)) break;
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
       for (int cc = 32 * half; cc < t.n; cc += 64) {
-        uint32_t u[32], v[32];
-        sm100::tmem_ld_32x32b_x32(tbase + cc, u);
-        sm100::tmem_ld_32x32b_x32(tbase + 256u + cc, v);
-        emit<OUT>(&staging[warp - 4], p, t, cc, col0, lane, [&](int i, float xs) {
-          return silu_times<OUT>((float)(int)u[i] * (xs * ws1), (float)(int)v[i] * (xs * ws3));
-        });
+        if constexpr (sizeof(OUT) == 2) {
+          stage_scales(stg, p, t, cc, lane);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+            uint32_t ulo[8], uhi[8], vlo[8], vhi[8];
+            const uint32_t c = tbase + cc + 16 * h;
+            sm100::tmem_ld_16x256b_x2(c, ulo);
+            sm100::tmem_ld_16x256b_x2(c + (16u << 16), uhi);
+            sm100::tmem_ld_16x256b_x2(c + 256u, vlo);
+            sm100::tmem_ld_16x256b_x2(c + 256u + (16u << 16), vhi);
+            sm100::tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float2 xs =
+                  *reinterpret_cast<const float2*>(&stg->scale[16 * h + 8 * j + 2 * (lane & 3)]);
+              uint32_t r[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int at = 4 * j + 2 * (k & 1);
+                const uint32_t *uu = (k < 2 ? ulo : uhi) + at, *vv = (k < 2 ? vlo : vhi) + at;
+                const float2 u = scaled(uu[0], uu[1], pair_scale(xs, ws1[k]));
+                const float2 v = scaled(vv[0], vv[1], pair_scale(xs, ws3[k]));
+                r[k] = pack_bf16x2(silu_times<OUT>(u.x, v.x), silu_times<OUT>(u.y, v.y));
+              }
+              sm100::stmatrix_x4_trans(blk + (2 * h + j) * 8 * kStagePitch, r);
+            }
+          }
+          store_staged(stg, p, t, cc, col0, lane);
+        } else {
+          uint32_t u[32], v[32];
+          sm100::tmem_ld_32x32b_x32(tbase + cc, u);
+          sm100::tmem_ld_32x32b_x32(tbase + 256u + cc, v);
+          sm100::tmem_ld_wait();
+          emit_f32(p, t, cc, col0, lane, [&](int i, float xs) {
+            return silu_times<OUT>((float)(int)u[i] * (xs * ws1[0]),
+                                   (float)(int)v[i] * (xs * ws3[0]));
+          });
+        }
       }
       sm100::tc_fence_before();
       sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty), 0));
