@@ -235,7 +235,7 @@ __device__ __forceinline__ float silu_times(float u, float v) {
 constexpr int kStagePitch = 80;
 struct Staging {
   unsigned char v[32 * kStagePitch];  // [32 rows][32 channels] bf16
-  float scale[32];                    // the rows' scales
+  float scale[kMaxTok];               // the scales of a tile's rows
 };
 
 // this lane's place in a stmatrix of one 8-row block
@@ -266,10 +266,14 @@ __device__ __forceinline__ void store_staged(const Staging* s, const I8Params& p
   __syncwarp();
 }
 
-// the scales of rows cc + [0, 32) of the tile
-__device__ __forceinline__ void stage_scales(Staging* s, const I8Params& p, const Tile& t, int cc,
+// the scales of the tile's rows, before the tile is there
+__device__ __forceinline__ void stage_scales(Staging* s, const I8Params& p, const Tile& t,
                                              int lane) {
-  s->scale[lane] = cc + lane < t.valid ? p.x_scale[t.row + cc + lane] : 0.0f;
+#pragma unroll
+  for (int k = 0; k < kMaxTok / 32; ++k) {
+    const int j = 32 * k + lane;
+    if (32 * k < t.n) s->scale[j] = j < t.valid ? p.x_scale[t.row + j] : 0.0f;
+  }
   __syncwarp();
 }
 
@@ -284,17 +288,36 @@ __device__ __forceinline__ void channel_scales(float (&ws)[4], const float* scal
   }
 }
 
+// 32 rows x 32 channels of the tile from the accumulator's fragments `lo`
+// (lanes 0-15 of the quadrant) and `hi` (16-31): scaled, activated, staged
+template <int ACT>
+__device__ __forceinline__ void stage_rows(Staging* s, uint32_t blk, const uint32_t (&lo)[16],
+                                           const uint32_t (&hi)[16], const float (&ws)[4], int cc,
+                                           int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 xs = *reinterpret_cast<const float2*>(&s->scale[cc + 8 * j + 2 * (lane & 3)]);
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t* v = (k < 2 ? lo : hi) + 4 * j + 2 * (k & 1);
+      const float2 u = scaled(v[0], v[1], pair_scale(xs, ws[k]));
+      r[k] = pack_bf16x2(activate<ACT>(u.x), activate<ACT>(u.y));
+    }
+    sm100::stmatrix_x4_trans(blk + j * 8 * kStagePitch, r);
+  }
+}
+
 // fp32 outputs: a lane keeps its channel, and the warp writes the 128
 // consecutive bytes of a row's 32 channels: value(i, x_scale of row i)
 template <class F>
-__device__ __forceinline__ void emit_f32(const I8Params& p, const Tile& t, int cc, int col0,
-                                         int lane, const F& value) {
-  const float mine = cc + lane < t.valid ? p.x_scale[t.row + cc + lane] : 0.0f;
+__device__ __forceinline__ void emit_f32(const Staging* s, const I8Params& p, const Tile& t,
+                                         int cc, int col0, int lane, const F& value) {
   float* out = static_cast<float*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
   const bool real = col0 + lane < p.n_out;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    const float r = value(i, __shfl_sync(~0u, mine, i));
+    const float r = value(i, s->scale[cc + i]);
     if (real && cc + i < t.valid) out[(size_t)i * p.n_out + lane] = r;
   }
 }
@@ -435,37 +458,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         ws[0] = col0 + lane < p.n_out ? p.w_scale[(size_t)t.group * p.n_out + col0 + lane] : 0.0f;
       }
+      stage_scales(stg, p, t, lane);
       if (!wait<true>(&st->tfull[sx], (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x64))
         break;
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(sx * 256);
-#pragma unroll 1
-      for (int cc = 0; cc < t.n; cc += 32) {
-        if constexpr (sizeof(OUT) == 2) {
-          uint32_t lo[16], hi[16];  // lanes 0-15 and 16-31 of the quadrant
-          sm100::tmem_ld_16x256b_x4(tbase + cc, lo);
-          sm100::tmem_ld_16x256b_x4(tbase + (16u << 16) + cc, hi);
-          stage_scales(stg, p, t, cc, lane);
-          sm100::tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 xs =
-                *reinterpret_cast<const float2*>(&stg->scale[8 * j + 2 * (lane & 3)]);
-            uint32_t r[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t* v = (k < 2 ? lo : hi) + 4 * j + 2 * (k & 1);
-              const float2 u = scaled(v[0], v[1], pair_scale(xs, ws[k]));
-              r[k] = pack_bf16x2(activate<ACT>(u.x), activate<ACT>(u.y));
-            }
-            sm100::stmatrix_x4_trans(blk + j * 8 * kStagePitch, r);
-          }
+      if constexpr (sizeof(OUT) == 2) {
+        // the next 32 rows are on their way from TMEM while these are written
+        uint32_t lo[2][16], hi[2][16];
+        auto fetch = [&](int b, int cc) {
+          sm100::tmem_ld_16x256b_x4(tbase + cc, lo[b]);
+          sm100::tmem_ld_16x256b_x4(tbase + (16u << 16) + cc, hi[b]);
+        };
+        auto give = [&](int b, int cc) {
+          stage_rows<ACT>(stg, blk, lo[b], hi[b], ws, cc, lane);
           store_staged(stg, p, t, cc, col0, lane);
-        } else {
+        };
+        fetch(0, 0);
+#pragma unroll 1
+        for (int cc = 0; cc < t.n; cc += 64) {
+          sm100::tmem_ld_wait();
+          if (cc + 32 < t.n) fetch(1, cc + 32);
+          give(0, cc);
+          if (cc + 32 >= t.n) break;
+          sm100::tmem_ld_wait();
+          if (cc + 64 < t.n) fetch(0, cc + 64);
+          give(1, cc + 32);
+        }
+      } else {
+#pragma unroll 1
+        for (int cc = 0; cc < t.n; cc += 32) {
           uint32_t v[32];
           sm100::tmem_ld_32x32b_x32(tbase + cc, v);
           sm100::tmem_ld_wait();
-          emit_f32(p, t, cc, col0, lane, [&](int i, float xs) {
+          emit_f32(stg, p, t, cc, col0, lane, [&](int i, float xs) {
             return activate<ACT>((float)(int)v[i] * (xs * ws[0]));
           });
         }
@@ -625,13 +651,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ws1[0] = real ? p.w_scale[wi] : 0.0f;
         ws3[0] = real ? p.w3_scale[wi] : 0.0f;
       }
+      stage_scales(stg, p, t, lane);
       if (!wait<true>(&st->tfull, (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x74)) break;
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
       for (int cc = 32 * half; cc < t.n; cc += 64) {
         if constexpr (sizeof(OUT) == 2) {
-          stage_scales(stg, p, t, cc, lane);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // 16 rows at a time
             uint32_t ulo[8], uhi[8], vlo[8], vhi[8];
@@ -644,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float2 xs =
-                  *reinterpret_cast<const float2*>(&stg->scale[16 * h + 8 * j + 2 * (lane & 3)]);
+                  *reinterpret_cast<const float2*>(&stg->scale[cc + 16 * h + 8 * j + 2 * (lane & 3)]);
               uint32_t r[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -663,7 +689,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sm100::tmem_ld_32x32b_x32(tbase + cc, u);
           sm100::tmem_ld_32x32b_x32(tbase + 256u + cc, v);
           sm100::tmem_ld_wait();
-          emit_f32(p, t, cc, col0, lane, [&](int i, float xs) {
+          emit_f32(stg, p, t, cc, col0, lane, [&](int i, float xs) {
             return silu_times<OUT>((float)(int)u[i] * (xs * ws1[0]),
                                    (float)(int)v[i] * (xs * ws3[0]));
           });
