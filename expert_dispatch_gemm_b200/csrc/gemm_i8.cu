@@ -227,20 +227,18 @@ __device__ __forceinline__ float silu_times(float u, float v) {
 // the output is a column of it, so a tile has to be transposed on its way out.
 // The accumulator is read as MMA fragments (two neighbouring rows of a channel
 // in a thread): they are scaled as pairs, converted as pairs and stored as 8 x
-// 8 blocks, transposed by stmatrix, into the warp's staging buffer, from which
-// each row's 32 channels leave as 16-byte stores. 1/8 of the shared-memory
-// stores and about a third of the instructions that storing one element at a
-// time takes. Rows are 80 bytes apart, so that the eight 16-byte pieces of a
-// block lie in different banks.
-constexpr int kStagePitch = 80;
+// 8 blocks, transposed by stmatrix, into the warp's staging buffer of 32 rows x
+// 32 channels, which leaves as one TMA store (rows past the group's last: as
+// 16-byte stores of the others). The buffer is laid out in the 64-byte swizzle,
+// in which the eight 16-byte pieces of a block lie in different banks.
 struct Staging {
-  unsigned char v[32 * kStagePitch];  // [32 rows][32 channels] bf16
-  float scale[kMaxTok];               // the scales of a tile's rows
+  unsigned char v[32 * 64];  // [32 rows][32 channels] bf16, swizzled
 };
-
-// this lane's place in a stmatrix of one 8-row block
-__device__ __forceinline__ uint32_t block_addr(const Staging* s, int lane) {
-  return sm100::smem_addr(s->v) + (lane & 7) * kStagePitch + (lane >> 3) * 16;
+struct Scales {
+  float x[kMaxTok];  // of a tile's rows
+};
+__device__ __forceinline__ uint32_t swizzled(int row, int piece) {
+  return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
 __device__ __forceinline__ float2 scaled(uint32_t a, uint32_t b, float2 s) {
@@ -250,31 +248,53 @@ __device__ __forceinline__ float2 pair_scale(float2 xs, float ws) {
   return __fmul2_rn(xs, make_float2(ws, ws));
 }
 
-// the staged rows [0, 32) to rows cc .. of the tile
-__device__ __forceinline__ void store_staged(const Staging* s, const I8Params& p, const Tile& t,
-                                             int cc, int col0, int lane) {
+// The 8 x 8 blocks r[j][k] (rows 8 j .., channels 8 k ..) of rows cc .. cc + 31 of
+// the tile to the output, through the staging buffer.
+__device__ __forceinline__ void write_rows(Staging* s, const CUtensorMap* to, const I8Params& p,
+                                           const Tile& t, int cc, int col0, int lane,
+                                           const uint32_t (&r)[4][4]) {
+  if (lane == 0) sm100::bulk_wait_read_all();  // the last store has read the buffer
   __syncwarp();
-  __nv_bfloat16* out =
-      static_cast<__nv_bfloat16*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
+  const uint32_t at = sm100::smem_addr(s->v) + swizzled(lane & 7, lane >> 3);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int i = k * 8 + (lane >> 2), c = lane & 3;
-    const uint4 v = *reinterpret_cast<const uint4*>(s->v + i * kStagePitch + c * 16);
-    if (cc + i < t.valid && col0 + c * 8 < p.n_out)
-      *reinterpret_cast<uint4*>(out + (size_t)i * p.n_out + c * 8) = v;
+  for (int j = 0; j < 4; ++j) sm100::stmatrix_x4_trans(at + j * 512, r[j]);
+  if (cc + 32 <= t.valid) {
+    sm100::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && col0 < p.n_out) {
+      sm100::tma_store_2d(to, col0, t.row + cc, s->v);
+      sm100::bulk_commit_group();
+    }
+  } else {
+    __syncwarp();
+    __nv_bfloat16* out =
+        static_cast<__nv_bfloat16*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = k * 8 + (lane >> 2), c = lane & 3;
+      const uint4 v = *reinterpret_cast<const uint4*>(s->v + swizzled(i, c));
+      if (cc + i < t.valid && col0 + c * 8 < p.n_out)
+        *reinterpret_cast<uint4*>(out + (size_t)i * p.n_out + c * 8) = v;
+    }
   }
-  __syncwarp();
 }
 
 // the scales of the tile's rows, before the tile is there
-__device__ __forceinline__ void stage_scales(Staging* s, const I8Params& p, const Tile& t,
+__device__ __forceinline__ void stage_scales(Scales* s, const I8Params& p, const Tile& t,
                                              int lane) {
+  __syncwarp();
 #pragma unroll
   for (int k = 0; k < kMaxTok / 32; ++k) {
     const int j = 32 * k + lane;
-    if (32 * k < t.n) s->scale[j] = j < t.valid ? p.x_scale[t.row + j] : 0.0f;
+    if (32 * k < t.n) s->x[j] = j < t.valid ? p.x_scale[t.row + j] : 0.0f;
   }
   __syncwarp();
+}
+// of rows cc + 8 j + 2 (lane % 4), + 1
+__device__ __forceinline__ void row_scales(float2 (&xs)[4], const Scales* s, int cc, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    xs[j] = *reinterpret_cast<const float2*>(&s->x[cc + 8 * j + 2 * (lane & 3)]);
 }
 
 // the scales of a thread's channels lane / 4 + 8 k of the warp's 32 from col0 on
@@ -289,35 +309,31 @@ __device__ __forceinline__ void channel_scales(float (&ws)[4], const float* scal
 }
 
 // 32 rows x 32 channels of the tile from the accumulator's fragments `lo`
-// (lanes 0-15 of the quadrant) and `hi` (16-31): scaled, activated, staged
+// (lanes 0-15 of the quadrant) and `hi` (16-31)
 template <int ACT>
-__device__ __forceinline__ void stage_rows(Staging* s, uint32_t blk, const uint32_t (&lo)[16],
-                                           const uint32_t (&hi)[16], const float (&ws)[4], int cc,
-                                           int lane) {
+__device__ __forceinline__ void finish(uint32_t (&r)[4][4], const uint32_t (&lo)[16],
+                                       const uint32_t (&hi)[16], const float2 (&xs)[4],
+                                       const float (&ws)[4]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 xs = *reinterpret_cast<const float2*>(&s->scale[cc + 8 * j + 2 * (lane & 3)]);
-    uint32_t r[4];
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t* v = (k < 2 ? lo : hi) + 4 * j + 2 * (k & 1);
-      const float2 u = scaled(v[0], v[1], pair_scale(xs, ws[k]));
-      r[k] = pack_bf16x2(activate<ACT>(u.x), activate<ACT>(u.y));
+      const float2 u = scaled(v[0], v[1], pair_scale(xs[j], ws[k]));
+      r[j][k] = pack_bf16x2(activate<ACT>(u.x), activate<ACT>(u.y));
     }
-    sm100::stmatrix_x4_trans(blk + j * 8 * kStagePitch, r);
-  }
 }
 
 // fp32 outputs: a lane keeps its channel, and the warp writes the 128
 // consecutive bytes of a row's 32 channels: value(i, x_scale of row i)
 template <class F>
-__device__ __forceinline__ void emit_f32(const Staging* s, const I8Params& p, const Tile& t,
+__device__ __forceinline__ void emit_f32(const Scales* s, const I8Params& p, const Tile& t,
                                          int cc, int col0, int lane, const F& value) {
   float* out = static_cast<float*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
   const bool real = col0 + lane < p.n_out;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    const float r = value(i, s->scale[cc + i]);
+    const float r = value(i, s->x[cc + i]);
     if (real && cc + i < t.valid) out[(size_t)i * p.n_out + lane] = r;
   }
 }
@@ -325,14 +341,14 @@ __device__ __forceinline__ void emit_f32(const Staging* s, const I8Params& p, co
 template <typename OUT, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     i8_pair_kernel(const __grid_constant__ RowMaps tx, const __grid_constant__ CUtensorMap tw,
-                   const I8Params p) {
+                   const __grid_constant__ CUtensorMap to, const I8Params p) {
   extern __shared__ __align__(1024) unsigned char ism[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(ism) + 1023) & ~uintptr_t(1023));
   constexpr int kRing = kStreams * kStagesS * kStageBytesS;
-  StreamState* st = reinterpret_cast<StreamState*>(base + kRing);
-  Staging* staging = reinterpret_cast<Staging*>(
-      base + kRing + ((sizeof(StreamState) + 127) & ~size_t(127)));
+  Staging* staging = reinterpret_cast<Staging*>(base + kRing);
+  Scales* scales = reinterpret_cast<Scales*>(staging + kEpiWarps);
+  StreamState* st = reinterpret_cast<StreamState*>(scales + kEpiWarps);
   auto sW = [&](int sx, int j) { return base + (sx * kStagesS + j) * kStageBytesS; };
   auto sX = [&](int sx, int j) { return sW(sx, j) + kWBytes; };
 
@@ -447,7 +463,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // and walks the tile's rows, 32 at a time
     const int q = warp & 3;
     Staging* stg = staging + (warp - 4);
-    const uint32_t blk = block_addr(stg, lane);
+    Scales* xsc = scales + (warp - 4);
     int local = 0;
     for (int tile = first; tile < total; tile += step, ++local) {
       const Tile t = decode(tile, p, st->g);
@@ -458,7 +474,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         ws[0] = col0 + lane < p.n_out ? p.w_scale[(size_t)t.group * p.n_out + col0 + lane] : 0.0f;
       }
-      stage_scales(stg, p, t, lane);
+      stage_scales(xsc, p, t, lane);
       if (!wait<true>(&st->tfull[sx], (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x64))
         break;
       sm100::tc_fence_after();
@@ -470,17 +486,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sm100::tmem_ld_16x256b_x4(tbase + cc, lo[b]);
           sm100::tmem_ld_16x256b_x4(tbase + (16u << 16) + cc, hi[b]);
         };
+        float2 xs[4];
+        uint32_t r[4][4];
         auto give = [&](int b, int cc) {
-          stage_rows<ACT>(stg, blk, lo[b], hi[b], ws, cc, lane);
-          store_staged(stg, p, t, cc, col0, lane);
+          finish<ACT>(r, lo[b], hi[b], xs, ws);
+          write_rows(stg, &to, p, t, cc, col0, lane, r);
         };
         fetch(0, 0);
 #pragma unroll 1
         for (int cc = 0; cc < t.n; cc += 64) {
+          row_scales(xs, xsc, cc, lane);
           sm100::tmem_ld_wait();
           if (cc + 32 < t.n) fetch(1, cc + 32);
           give(0, cc);
           if (cc + 32 >= t.n) break;
+          row_scales(xs, xsc, cc + 32, lane);
           sm100::tmem_ld_wait();
           if (cc + 64 < t.n) fetch(0, cc + 64);
           give(1, cc + 32);
@@ -491,7 +511,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t v[32];
           sm100::tmem_ld_32x32b_x32(tbase + cc, v);
           sm100::tmem_ld_wait();
-          emit_f32(stg, p, t, cc, col0, lane, [&](int i, float xs) {
+          emit_f32(xsc, p, t, cc, col0, lane, [&](int i, float xs) {
             return activate<ACT>((float)(int)v[i] * (xs * ws[0]));
           });
         }
@@ -499,6 +519,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty[sx]), 0));
     }
+    if (lane == 0) sm100::bulk_wait_all();
   }
   sm100::tc_fence_before();
   __syncthreads();
@@ -513,14 +534,15 @@ template <typename OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     i8_swiglu_pair_kernel(const __grid_constant__ RowMaps tx,
                           const __grid_constant__ CUtensorMap tw,
-                          const __grid_constant__ CUtensorMap tw3, const I8Params p) {
+                          const __grid_constant__ CUtensorMap tw3,
+                          const __grid_constant__ CUtensorMap to, const I8Params p) {
   extern __shared__ __align__(1024) unsigned char ism[];
   unsigned char* base = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(ism) + 1023) & ~uintptr_t(1023));
   constexpr int kRing = kStagesU * kStageBytesU;
-  UpState* st = reinterpret_cast<UpState*>(base + kRing);
-  Staging* staging = reinterpret_cast<Staging*>(
-      base + kRing + ((sizeof(UpState) + 127) & ~size_t(127)));
+  Staging* staging = reinterpret_cast<Staging*>(base + kRing);
+  Scales* scales = reinterpret_cast<Scales*>(staging + kEpiWarps);
+  UpState* st = reinterpret_cast<UpState*>(scales + kEpiWarps);
   auto sW = [&](int j, int which) { return base + j * kStageBytesU + which * kWBytes; };
   auto sX = [&](int j) { return base + j * kStageBytesU + 2 * kWBytes; };
 
@@ -636,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3;
     const int half = (warp - 4) >> 2;
     Staging* stg = staging + (warp - 4);
-    const uint32_t blk = block_addr(stg, lane);
+    Scales* xsc = scales + (warp - 4);
     int local = 0;
     for (int tile = pair_id; tile < total; tile += num_pairs, ++local) {
       const Tile t = decode(tile, p, st->g);
@@ -651,13 +673,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ws1[0] = real ? p.w_scale[wi] : 0.0f;
         ws3[0] = real ? p.w3_scale[wi] : 0.0f;
       }
-      stage_scales(stg, p, t, lane);
+      stage_scales(xsc, p, t, lane);
       if (!wait<true>(&st->tfull, (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x74)) break;
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
       for (int cc = 32 * half; cc < t.n; cc += 64) {
         if constexpr (sizeof(OUT) == 2) {
+          float2 xs[4];
+          row_scales(xs, xsc, cc, lane);
+          uint32_t r[4][4];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {  // 16 rows at a time
             uint32_t ulo[8], uhi[8], vlo[8], vhi[8];
@@ -668,28 +693,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             sm100::tmem_ld_16x256b_x2(c + 256u + (16u << 16), vhi);
             sm100::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float2 xs =
-                  *reinterpret_cast<const float2*>(&stg->scale[cc + 16 * h + 8 * j + 2 * (lane & 3)]);
-              uint32_t r[4];
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const int at = 4 * j + 2 * (k & 1);
                 const uint32_t *uu = (k < 2 ? ulo : uhi) + at, *vv = (k < 2 ? vlo : vhi) + at;
-                const float2 u = scaled(uu[0], uu[1], pair_scale(xs, ws1[k]));
-                const float2 v = scaled(vv[0], vv[1], pair_scale(xs, ws3[k]));
-                r[k] = pack_bf16x2(silu_times<OUT>(u.x, v.x), silu_times<OUT>(u.y, v.y));
+                const float2 u = scaled(uu[0], uu[1], pair_scale(xs[2 * h + j], ws1[k]));
+                const float2 v = scaled(vv[0], vv[1], pair_scale(xs[2 * h + j], ws3[k]));
+                r[2 * h + j][k] = pack_bf16x2(silu_times<OUT>(u.x, v.x), silu_times<OUT>(u.y, v.y));
               }
-              sm100::stmatrix_x4_trans(blk + (2 * h + j) * 8 * kStagePitch, r);
-            }
           }
-          store_staged(stg, p, t, cc, col0, lane);
+          write_rows(stg, &to, p, t, cc, col0, lane, r);
         } else {
           uint32_t u[32], v[32];
           sm100::tmem_ld_32x32b_x32(tbase + cc, u);
           sm100::tmem_ld_32x32b_x32(tbase + 256u + cc, v);
           sm100::tmem_ld_wait();
-          emit_f32(stg, p, t, cc, col0, lane, [&](int i, float xs) {
+          emit_f32(xsc, p, t, cc, col0, lane, [&](int i, float xs) {
             return silu_times<OUT>((float)(int)u[i] * (xs * ws1[0]),
                                    (float)(int)v[i] * (xs * ws3[0]));
           });
@@ -698,6 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty), 0));
     }
+    if (lane == 0) sm100::bulk_wait_all();
   }
   sm100::tc_fence_before();
   __syncthreads();
@@ -745,9 +766,21 @@ bool byte_map(CUtensorMap* m, const void* ptr, long long rows, long long cols, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// the output [rows, cols] bf16 for stores of 32 x 32, 64-byte swizzle
+bool out_map(CUtensorMap* m, void* ptr, long long rows, long long cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t gstride[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t box[2] = {32, 32}, estride[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, gdim, gstride, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <class State>
 constexpr size_t smem_bytes(int ring) {
-  return (size_t)ring + ((sizeof(State) + 127) & ~size_t(127)) + kEpiWarps * sizeof(Staging) + 1024;
+  return (size_t)ring + kEpiWarps * (sizeof(Staging) + sizeof(Scales)) + sizeof(State) + 1024;
 }
 
 template <class K, class... Args>
@@ -759,20 +792,21 @@ cudaError_t launch_i8(K kern, int pairs, size_t bytes, cudaStream_t s, const Arg
 }
 
 template <typename OUT>
-cudaError_t run_gemm(const RowMaps& x, const CUtensorMap& w, const CUtensorMap& w3, int act,
-                     const I8Params& p, int pairs, cudaStream_t s) {
+cudaError_t run_gemm(const RowMaps& x, const CUtensorMap& w, const CUtensorMap& w3,
+                     const CUtensorMap& o, int act, const I8Params& p, int pairs,
+                     cudaStream_t s) {
   constexpr size_t stream_bytes = smem_bytes<StreamState>(kStreams * kStagesS * kStageBytesS);
   constexpr size_t up_bytes = smem_bytes<UpState>(kStagesU * kStageBytesU);
   static_assert(stream_bytes <= 232448 && up_bytes <= 232448, "227 KB of shared memory");
   switch (act) {
     case MOE_I8_SWIGLU:
-      return launch_i8(i8_swiglu_pair_kernel<OUT>, pairs, up_bytes, s, x, w, w3, p);
+      return launch_i8(i8_swiglu_pair_kernel<OUT>, pairs, up_bytes, s, x, w, w3, o, p);
     case MOE_I8_RELU:
-      return launch_i8(i8_pair_kernel<OUT, A_RELU>, pairs, stream_bytes, s, x, w, p);
+      return launch_i8(i8_pair_kernel<OUT, A_RELU>, pairs, stream_bytes, s, x, w, o, p);
     case MOE_I8_GELU:
-      return launch_i8(i8_pair_kernel<OUT, A_GELU>, pairs, stream_bytes, s, x, w, p);
+      return launch_i8(i8_pair_kernel<OUT, A_GELU>, pairs, stream_bytes, s, x, w, o, p);
     default:
-      return launch_i8(i8_pair_kernel<OUT, A_NONE>, pairs, stream_bytes, s, x, w, p);
+      return launch_i8(i8_pair_kernel<OUT, A_NONE>, pairs, stream_bytes, s, x, w, o, p);
   }
 }
 
@@ -832,6 +866,9 @@ moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq, const fl
   if (!byte_map(&mw, w, wrows, cfg->k, 128)) return MOE_ERR_CUDA;
   mw3 = mw;
   if (swiglu && !byte_map(&mw3, w3, wrows, cfg->k, 128)) return MOE_ERR_CUDA;
+  // (fp32 outputs are not stored through it)
+  CUtensorMap mo = mw;
+  if (cfg->dtype == MOE_BF16 && !out_map(&mo, out, cfg->rows, cfg->n_out)) return MOE_ERR_CUDA;
   I8Params p{};
   p.starts = starts;
   p.counts = counts;
@@ -850,8 +887,8 @@ moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq, const fl
   const int pairs = (int)(most < kBlockSms / 2 ? most : kBlockSms / 2);
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = cfg->dtype == MOE_BF16
-                            ? run_gemm<__nv_bfloat16>(x, mw, mw3, cfg->act, p, pairs, s)
-                            : run_gemm<float>(x, mw, mw3, cfg->act, p, pairs, s);
+                            ? run_gemm<__nv_bfloat16>(x, mw, mw3, mo, cfg->act, p, pairs, s)
+                            : run_gemm<float>(x, mw, mw3, mo, cfg->act, p, pairs, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
