@@ -24,10 +24,10 @@
 // - i8_pair_kernel: two tile streams, each with its own producer, ring and
 //   256-column accumulator; while one stream's epilogue drains, the other
 //   keeps the pipe busy.
-//     warps 0 / 2 producers, 1 / 3 issuers, 4-11 epilogue (four a stream)
+//     warps 0 / 2 producers, 1 / 3 issuers, 4-19 epilogue (eight a stream)
 // - i8_swiglu_pair_kernel: one stream, W1 and W3 rows as two A operands of a
 //   stage, u and v into two accumulators that meet in one epilogue thread.
-//     warp 0 producer, 1 / 2 issuers, 4-11 epilogue
+//     warp 0 producer, 1 / 2 issuers, 4-19 epilogue
 // Every mbarrier wait is bounded; on a timeout a role records the error, its
 // copies and MMAs in flight are waited for (bounded), TMEM is freed and the
 // kernel returns.
@@ -50,7 +50,7 @@ constexpr int kWBytes = 128 * kBK;          // this CTA's 128 channels
 constexpr int kXBytes = 128 * kBK;          // up to 128 rows
 constexpr int kMaxTok = 256;                // rows of a tile (MMA N)
 constexpr int kTokUnit = 32;                // N is a multiple of this (M = 256 pairs)
-constexpr int kEpiWarps = 8;
+constexpr int kEpiWarps = 16;
 constexpr int kThreads = 32 * (4 + kEpiWarps);
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
@@ -227,15 +227,16 @@ __device__ __forceinline__ float silu_times(float u, float v) {
 // the output is a column of it, so a tile has to be transposed on its way out.
 // The accumulator is read as MMA fragments (two neighbouring rows of a channel
 // in a thread): they are scaled as pairs, converted as pairs and stored as 8 x
-// 8 blocks, transposed by stmatrix, into the warp's staging buffer of 32 rows x
+// 8 blocks, transposed by stmatrix, into the warp's staging buffer of 16 rows x
 // 32 channels, which leaves as one TMA store (rows past the group's last: as
-// 16-byte stores of the others). The buffer is laid out in the 64-byte swizzle,
+// 16-byte stores of the others). Two warps take turns at the 32-row groups of
+// each TMEM lane quadrant. The buffer is laid out in the 64-byte swizzle,
 // in which the eight 16-byte pieces of a block lie in different banks.
 struct Staging {
-  unsigned char v[32 * 64];  // [32 rows][32 channels] bf16, swizzled
+  unsigned char v[16 * 64];  // [16 rows][32 channels] bf16, swizzled
 };
 struct Scales {
-  float x[kMaxTok];  // of a tile's rows
+  float x[kMaxTok / 2];  // of the rows of a tile that the warp takes: 32 of 64
 };
 __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
   return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
@@ -248,17 +249,17 @@ __device__ __forceinline__ float2 pair_scale(float2 xs, float ws) {
   return __fmul2_rn(xs, make_float2(ws, ws));
 }
 
-// The 8 x 8 blocks r[j][k] (rows 8 j .., channels 8 k ..) of rows cc .. cc + 31 of
+// The 8 x 8 blocks r[j][k] (rows 8 j .., channels 8 k ..) of rows cc .. cc + 15 of
 // the tile to the output, through the staging buffer.
 __device__ __forceinline__ void write_rows(Staging* s, const CUtensorMap* to, const I8Params& p,
                                            const Tile& t, int cc, int col0, int lane,
-                                           const uint32_t (&r)[4][4]) {
+                                           const uint32_t (&r)[2][4]) {
   if (lane == 0) sm100::bulk_wait_read_all();  // the last store has read the buffer
   __syncwarp();
   const uint32_t at = sm100::smem_addr(s->v) + swizzled(lane & 7, lane >> 3);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) sm100::stmatrix_x4_trans(at + j * 512, r[j]);
-  if (cc + 32 <= t.valid) {
+  for (int j = 0; j < 2; ++j) sm100::stmatrix_x4_trans(at + j * 512, r[j]);
+  if (cc + 16 <= t.valid) {
     sm100::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && col0 < p.n_out) {
@@ -270,7 +271,7 @@ __device__ __forceinline__ void write_rows(Staging* s, const CUtensorMap* to, co
     __nv_bfloat16* out =
         static_cast<__nv_bfloat16*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 2; ++k) {
       const int i = k * 8 + (lane >> 2), c = lane & 3;
       const uint4 v = *reinterpret_cast<const uint4*>(s->v + swizzled(i, c));
       if (cc + i < t.valid && col0 + c * 8 < p.n_out)
@@ -279,22 +280,19 @@ __device__ __forceinline__ void write_rows(Staging* s, const CUtensorMap* to, co
   }
 }
 
-// the scales of the tile's rows, before the tile is there
+// the scales of the tile's rows 64 k + 32 half + [0, 32), before the tile is there
 __device__ __forceinline__ void stage_scales(Scales* s, const I8Params& p, const Tile& t,
-                                             int lane) {
+                                             int half, int lane) {
   __syncwarp();
 #pragma unroll
-  for (int k = 0; k < kMaxTok / 32; ++k) {
-    const int j = 32 * k + lane;
-    if (32 * k < t.n) s->x[j] = j < t.valid ? p.x_scale[t.row + j] : 0.0f;
+  for (int k = 0; k < kMaxTok / 64; ++k) {
+    const int j = 64 * k + 32 * half + lane;
+    if (64 * k < t.n) s->x[32 * k + lane] = j < t.valid ? p.x_scale[t.row + j] : 0.0f;
   }
   __syncwarp();
 }
-// of rows cc + 8 j + 2 (lane % 4), + 1
-__device__ __forceinline__ void row_scales(float2 (&xs)[4], const Scales* s, int cc, int lane) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    xs[j] = *reinterpret_cast<const float2*>(&s->x[cc + 8 * j + 2 * (lane & 3)]);
+__device__ __forceinline__ const float* scales_at(const Scales* s, int cc) {
+  return s->x + (cc >> 6) * 32 + (cc & 31);  // of row cc of the tile
 }
 
 // the scales of a thread's channels lane / 4 + 8 k of the warp's 32 from col0 on
@@ -308,32 +306,53 @@ __device__ __forceinline__ void channel_scales(float (&ws)[4], const float* scal
   }
 }
 
-// 32 rows x 32 channels of the tile from the accumulator's fragments `lo`
+// 16 rows x 32 channels of the tile from the accumulator's fragments `lo`
 // (lanes 0-15 of the quadrant) and `hi` (16-31)
 template <int ACT>
-__device__ __forceinline__ void finish(uint32_t (&r)[4][4], const uint32_t (&lo)[16],
-                                       const uint32_t (&hi)[16], const float2 (&xs)[4],
-                                       const float (&ws)[4]) {
+__device__ __forceinline__ void finish(uint32_t (&r)[2][4], const uint32_t (&lo)[8],
+                                       const uint32_t (&hi)[8], const float* xs,
+                                       const float (&ws)[4], int lane) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 2; ++j) {
+    const float2 x = *reinterpret_cast<const float2*>(xs + 8 * j + 2 * (lane & 3));
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t* v = (k < 2 ? lo : hi) + 4 * j + 2 * (k & 1);
-      const float2 u = scaled(v[0], v[1], pair_scale(xs[j], ws[k]));
+      const float2 u = scaled(v[0], v[1], pair_scale(x, ws[k]));
       r[j][k] = pack_bf16x2(activate<ACT>(u.x), activate<ACT>(u.y));
     }
+  }
+}
+__device__ __forceinline__ void finish_gated(uint32_t (&r)[2][4], const uint32_t (&ulo)[8],
+                                             const uint32_t (&uhi)[8], const uint32_t (&vlo)[8],
+                                             const uint32_t (&vhi)[8], const float* xs,
+                                             const float (&ws1)[4], const float (&ws3)[4],
+                                             int lane) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float2 x = *reinterpret_cast<const float2*>(xs + 8 * j + 2 * (lane & 3));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = 4 * j + 2 * (k & 1);
+      const uint32_t *uu = (k < 2 ? ulo : uhi) + at, *vv = (k < 2 ? vlo : vhi) + at;
+      const float2 u = scaled(uu[0], uu[1], pair_scale(x, ws1[k]));
+      const float2 v = scaled(vv[0], vv[1], pair_scale(x, ws3[k]));
+      r[j][k] = pack_bf16x2(silu_times<__nv_bfloat16>(u.x, v.x),
+                            silu_times<__nv_bfloat16>(u.y, v.y));
+    }
+  }
 }
 
 // fp32 outputs: a lane keeps its channel, and the warp writes the 128
 // consecutive bytes of a row's 32 channels: value(i, x_scale of row i)
-template <class F>
+template <int ROWS, class F>
 __device__ __forceinline__ void emit_f32(const Scales* s, const I8Params& p, const Tile& t,
                                          int cc, int col0, int lane, const F& value) {
   float* out = static_cast<float*>(p.out) + (size_t)(t.row + cc) * p.n_out + col0;
   const bool real = col0 + lane < p.n_out;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const float r = value(i, s->x[cc + i]);
+  for (int i = 0; i < ROWS; ++i) {
+    const float r = value(i, scales_at(s, cc)[i]);
     if (real && cc + i < t.valid) out[(size_t)i * p.n_out + lane] = r;
   }
 }
@@ -459,9 +478,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // epilogue of stream sx: warp q = warp % 4 owns lanes (channels) 32q..32q+31
-    // and walks the tile's rows, 32 at a time
-    const int q = warp & 3;
+    // epilogue of stream sx: warps q = warp % 4 own lanes (channels) 32q..32q+31,
+    // two of them for alternate 32-row groups of the tile
+    const int q = warp & 3, half = ((warp - 4) >> 2) & 1;
     Staging* stg = staging + (warp - 4);
     Scales* xsc = scales + (warp - 4);
     int local = 0;
@@ -474,44 +493,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         ws[0] = col0 + lane < p.n_out ? p.w_scale[(size_t)t.group * p.n_out + col0 + lane] : 0.0f;
       }
-      stage_scales(xsc, p, t, lane);
+      stage_scales(xsc, p, t, half, lane);
       if (!wait<true>(&st->tfull[sx], (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x64))
         break;
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(sx * 256);
       if constexpr (sizeof(OUT) == 2) {
-        // the next 32 rows are on their way from TMEM while these are written
-        uint32_t lo[2][16], hi[2][16];
+        // the next 16 rows are on their way from TMEM while these are written
+        uint32_t lo[2][8], hi[2][8], r[2][4];
         auto fetch = [&](int b, int cc) {
-          sm100::tmem_ld_16x256b_x4(tbase + cc, lo[b]);
-          sm100::tmem_ld_16x256b_x4(tbase + (16u << 16) + cc, hi[b]);
+          sm100::tmem_ld_16x256b_x2(tbase + cc, lo[b]);
+          sm100::tmem_ld_16x256b_x2(tbase + (16u << 16) + cc, hi[b]);
         };
-        float2 xs[4];
-        uint32_t r[4][4];
         auto give = [&](int b, int cc) {
-          finish<ACT>(r, lo[b], hi[b], xs, ws);
+          finish<ACT>(r, lo[b], hi[b], scales_at(xsc, cc), ws, lane);
           write_rows(stg, &to, p, t, cc, col0, lane, r);
         };
-        fetch(0, 0);
+        if (32 * half < t.n) fetch(0, 32 * half);
 #pragma unroll 1
-        for (int cc = 0; cc < t.n; cc += 64) {
-          row_scales(xs, xsc, cc, lane);
+        for (int cc = 32 * half; cc < t.n; cc += 64) {
           sm100::tmem_ld_wait();
-          if (cc + 32 < t.n) fetch(1, cc + 32);
+          fetch(1, cc + 16);
           give(0, cc);
-          if (cc + 32 >= t.n) break;
-          row_scales(xs, xsc, cc + 32, lane);
           sm100::tmem_ld_wait();
           if (cc + 64 < t.n) fetch(0, cc + 64);
-          give(1, cc + 32);
+          give(1, cc + 16);
         }
       } else {
 #pragma unroll 1
-        for (int cc = 0; cc < t.n; cc += 32) {
+        for (int cc = 32 * half; cc < t.n; cc += 64) {
           uint32_t v[32];
           sm100::tmem_ld_32x32b_x32(tbase + cc, v);
           sm100::tmem_ld_wait();
-          emit_f32(xsc, p, t, cc, col0, lane, [&](int i, float xs) {
+          emit_f32<32>(xsc, p, t, cc, col0, lane, [&](int i, float xs) {
             return activate<ACT>((float)(int)v[i] * (xs * ws[0]));
           });
         }
@@ -653,10 +667,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp >= 4) {
-    // epilogue: warps q and q + 4 own lanes 32q..32q+31 and take alternate
-    // 32-row groups; u in columns [0, 256), v in [256, 512)
+    // epilogue: warps q = warp % 4 own lanes 32q..32q+31, four of them: two for
+    // alternate 32-row groups, and of each group two for 16 rows each; u in columns
+    // [0, 256), v in [256, 512)
     const int q = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int half = ((warp - 4) >> 2) & 1, sub = (warp - 4) >> 3;
     Staging* stg = staging + (warp - 4);
     Scales* xsc = scales + (warp - 4);
     int local = 0;
@@ -673,43 +688,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ws1[0] = real ? p.w_scale[wi] : 0.0f;
         ws3[0] = real ? p.w3_scale[wi] : 0.0f;
       }
-      stage_scales(xsc, p, t, lane);
+      stage_scales(xsc, p, t, half, lane);
       if (!wait<true>(&st->tfull, (uint32_t)local & 1u, st, p.err, kErrGemmTimeout | 0x74)) break;
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
       for (int cc = 32 * half; cc < t.n; cc += 64) {
         if constexpr (sizeof(OUT) == 2) {
-          float2 xs[4];
-          row_scales(xs, xsc, cc, lane);
-          uint32_t r[4][4];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {  // 16 rows at a time
-            uint32_t ulo[8], uhi[8], vlo[8], vhi[8];
-            const uint32_t c = tbase + cc + 16 * h;
-            sm100::tmem_ld_16x256b_x2(c, ulo);
-            sm100::tmem_ld_16x256b_x2(c + (16u << 16), uhi);
-            sm100::tmem_ld_16x256b_x2(c + 256u, vlo);
-            sm100::tmem_ld_16x256b_x2(c + 256u + (16u << 16), vhi);
-            sm100::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int at = 4 * j + 2 * (k & 1);
-                const uint32_t *uu = (k < 2 ? ulo : uhi) + at, *vv = (k < 2 ? vlo : vhi) + at;
-                const float2 u = scaled(uu[0], uu[1], pair_scale(xs[2 * h + j], ws1[k]));
-                const float2 v = scaled(vv[0], vv[1], pair_scale(xs[2 * h + j], ws3[k]));
-                r[2 * h + j][k] = pack_bf16x2(silu_times<OUT>(u.x, v.x), silu_times<OUT>(u.y, v.y));
-              }
-          }
-          write_rows(stg, &to, p, t, cc, col0, lane, r);
-        } else {
-          uint32_t u[32], v[32];
-          sm100::tmem_ld_32x32b_x32(tbase + cc, u);
-          sm100::tmem_ld_32x32b_x32(tbase + 256u + cc, v);
+          uint32_t ulo[8], uhi[8], vlo[8], vhi[8], r[2][4];
+          const int at = cc + 16 * sub;
+          const uint32_t c = tbase + at;
+          sm100::tmem_ld_16x256b_x2(c, ulo);
+          sm100::tmem_ld_16x256b_x2(c + (16u << 16), uhi);
+          sm100::tmem_ld_16x256b_x2(c + 256u, vlo);
+          sm100::tmem_ld_16x256b_x2(c + 256u + (16u << 16), vhi);
           sm100::tmem_ld_wait();
-          emit_f32(xsc, p, t, cc, col0, lane, [&](int i, float xs) {
+          finish_gated(r, ulo, uhi, vlo, vhi, scales_at(xsc, at), ws1, ws3, lane);
+          write_rows(stg, &to, p, t, at, col0, lane, r);
+        } else {
+          uint32_t u[16], v[16];
+          const int at = cc + 16 * sub;
+          sm100::tmem_ld_32x32b_x16(tbase + at, u);
+          sm100::tmem_ld_32x32b_x16(tbase + 256u + at, v);
+          sm100::tmem_ld_wait();
+          emit_f32<16>(xsc, p, t, at, col0, lane, [&](int i, float xs) {
             return silu_times<OUT>((float)(int)u[i] * (xs * ws1[0]),
                                    (float)(int)v[i] * (xs * ws3[0]));
           });
@@ -766,13 +768,13 @@ bool byte_map(CUtensorMap* m, const void* ptr, long long rows, long long cols, i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// the output [rows, cols] bf16 for stores of 32 x 32, 64-byte swizzle
+// the output [rows, cols] bf16 for stores of 16 rows x 32 columns, 64-byte swizzle
 bool out_map(CUtensorMap* m, void* ptr, long long rows, long long cols) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t gstride[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t box[2] = {32, 32}, estride[2] = {1, 1};
+  const cuuint32_t box[2] = {32, 16}, estride[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, ptr, gdim, gstride, box, estride,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
