@@ -58,12 +58,13 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 constexpr int kStreams = 2, kStagesS = 3, kStageBytesS = kWBytes + kXBytes;  // 3 x 32 KB each
 constexpr int kStagesU = 4, kStageBytesU = 2 * kWBytes + kXBytes;            // 4 x 48 KB
 
-enum { A_NONE = MOE_I8_NONE, A_RELU = MOE_I8_RELU, A_GELU = MOE_I8_GELU };
+enum { A_NONE = MOE_I8_NONE, A_RELU = MOE_I8_RELU, A_GELU = MOE_I8_GELU, A_SWIGLU = MOE_I8_SWIGLU };
 
 struct I8Params {
   const int32_t *starts, *counts;  // NULL: one group of all rows
   const float *x_scale, *w_scale, *w3_scale;
   int groups, rows, K, n_out, mt_tiles;
+  int parts;  // of K, in the split kernel
   void* out;
   int* err;
 };
@@ -192,22 +193,20 @@ __device__ __forceinline__ Tile decode(int tile, const I8Params& p, const GroupT
   return t;
 }
 
-// A CTA's rows of the tile (N / 2, a multiple of 16): boxes of 128, 64, 32 and
-// 16 rows at 1 KB-aligned offsets, whole 8-row atoms of the swizzle.
-constexpr int kBoxes = 4;
+// A CTA's rows of the tile (N / 2, a multiple of 16): boxes of 64 and 16 rows at
+// 1 KB-aligned offsets, whole 8-row atoms of the swizzle. (Each more box size
+// would be one more tensor map for the host to encode a call.)
+constexpr int kBoxes = 2;
 struct RowMaps {
-  CUtensorMap m[kBoxes];  // box of 16 << b rows
+  CUtensorMap m[kBoxes];  // boxes of 16 and 64 rows
 };
 __device__ __forceinline__ void load_rows(unsigned char* dst, const RowMaps& x, uint32_t bar,
                                           int k, int row, int rows) {
   int off = 0;
-#pragma unroll
-  for (int b = kBoxes - 1; b >= 0; --b) {
-    if (rows & (16 << b)) {
-      sm100::tma_load_2d_pair(dst + off * kBK, &x.m[b], bar, k, row + off);
-      off += 16 << b;
-    }
-  }
+  for (; off + 64 <= rows; off += 64)
+    sm100::tma_load_2d_pair(dst + off * kBK, &x.m[1], bar, k, row + off);
+  for (; off < rows; off += 16)
+    sm100::tma_load_2d_pair(dst + off * kBK, &x.m[0], bar, k, row + off);
 }
 
 template <int ACT>
@@ -533,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty[sx]), 0));
     }
-    if (lane == 0) sm100::bulk_wait_all();
+    if (lane == 0) sm100::bulk_wait_read_all();
   }
   sm100::tc_fence_before();
   __syncthreads();
@@ -720,7 +719,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sm100::tc_fence_before();
       sm100::mbar_arrive_cluster(sm100::mapa_shared(sm100::smem_addr(&st->tempty), 0));
     }
-    if (lane == 0) sm100::bulk_wait_all();
+    if (lane == 0) sm100::bulk_wait_read_all();
   }
   sm100::tc_fence_before();
   __syncthreads();
@@ -728,6 +727,262 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == 1) {
     sm100::tc_fence_after();
     sm100::tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Few tiles (one decoded token, a small expert): the reduction split over the
+// pairs of a cluster, so that the weights stream through more SMs. One tile a
+// cluster; pair i of S takes K blocks [KB i / S, KB (i + 1) / S), with the whole
+// shared memory as its ring. The int32 sums are exact, so any split gives the
+// same result: the tile's 32-row chunks are dealt out to the pairs, each CTA
+// sends its sums of the others' chunks into their rings (free by then) through
+// distributed shared memory, adds what it received to its own, and writes.
+// One row, k 2048, 7,168 channels: see the measurements at the launch.
+// ---------------------------------------------------------------------------
+constexpr int kSplitRing = 192 * 1024;
+constexpr int kSplitStages = 6;  // of 32 KB; SwiGLU 4 of 48 KB
+struct SplitState {
+  uint64_t full[kSplitStages];
+  uint64_t empty[kSplitStages];
+  uint64_t tfull;
+  uint64_t drain[2];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  GroupTable g;
+};
+
+__device__ __forceinline__ void send16(uint32_t to, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+
+template <typename OUT, int ACT>
+__global__ void __launch_bounds__(kThreads, 1)
+    i8_split_kernel(const __grid_constant__ RowMaps tx, const __grid_constant__ CUtensorMap tw,
+                    const __grid_constant__ CUtensorMap tw3,
+                    const __grid_constant__ CUtensorMap to, const I8Params p) {
+  constexpr int SIDES = ACT == A_SWIGLU ? 2 : 1;
+  constexpr int STAGE = SIDES * kWBytes + kXBytes, STAGES = kSplitRing / STAGE;
+  constexpr int UNIT = 16 * 32 * 4;  // bytes of a warp's 16 rows x 32 channels of sums
+  extern __shared__ __align__(1024) unsigned char ism[];
+  unsigned char* base = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(ism) + 1023) & ~uintptr_t(1023));
+  Staging* staging = reinterpret_cast<Staging*>(base + kSplitRing);
+  Scales* scales = reinterpret_cast<Scales*>(staging + kEpiWarps);
+  SplitState* st = reinterpret_cast<SplitState*>(scales + kEpiWarps);
+  auto sW = [&](int j, int side) { return base + j * STAGE + side * kWBytes; };
+  auto sX = [&](int j) { return base + j * STAGE + SIDES * kWBytes; };
+
+  const uint32_t cta = sm100::cluster_ctarank();
+  const uint32_t rank = cta & 1, lead = cta & ~1u;
+  const bool leader = rank == 0;
+  const uint16_t pair_mask = (uint16_t)(0x3u << lead);
+  const int part = (int)(cta >> 1), parts = p.parts;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int j = 0; j < STAGES; ++j) {
+      sm100::mbar_init(&st->full[j], 1);
+      sm100::mbar_init(&st->empty[j], SIDES);
+    }
+    sm100::mbar_init(&st->tfull, SIDES);
+    sm100::mbar_init(&st->drain[0], 1);
+    sm100::mbar_init(&st->drain[1], 1);
+    st->abort_flag = 0;
+    sm100::fence_mbar_init();
+  }
+  if (warp == 0 && lane < kBoxes) sm100::tma_prefetch_desc(&tx.m[lane]);
+  if (warp == 0 && lane == kBoxes) sm100::tma_prefetch_desc(&tw);
+  if (SIDES == 2 && warp == 0 && lane == kBoxes + 1) sm100::tma_prefetch_desc(&tw3);
+  if (warp == 1) {
+    sm100::tmem_alloc_pair(&st->tmem_base, SIDES * 256);
+    sm100::tmem_relinquish_pair();
+  }
+  pdl_wait();
+  load_groups(st->g, p, tid);
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::cluster_sync();
+  sm100::tc_fence_after();
+  const uint32_t tmem = st->tmem_base;
+
+  const int tile = blockIdx.x / (2 * parts);
+  const bool live = tile < st->g.tiles[p.groups];  // (the same in the whole cluster)
+  const Tile t = live ? decode(tile, p, st->g) : Tile{0, 0, 0, 0, 0};
+  const int all = (p.K + kBK - 1) / kBK;
+  const int kb0 = all * part / parts, kb1 = live ? all * (part + 1) / parts : kb0;
+  // epilogue warps: quadrant q; units of 16 rows, unit u = 2 chunk + half, by warp set
+  const int q = warp & 3, set = (warp - 4) >> 2;
+  const int units = t.n / 16;
+  const int col0 = t.m0 + (int)rank * 128 + 32 * q;
+  Scales* xsc = scales + (warp - 4);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const int half = t.n / 2;
+      const uint32_t bytes = SIDES * kWBytes + (uint32_t)half * kBK;
+      const int wrow = t.group * p.n_out + t.m0 + (int)rank * 128;
+      const int xrow = t.row + (int)rank * half;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait<false>(&st->empty[stage], phase ^ 1u, st, p.err, kErrGemmTimeout | 0x81)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fl = sm100::mapa_shared(sm100::smem_addr(&st->full[stage]), lead);
+        if (leader) sm100::mbar_arrive_expect_tx(&st->full[stage], 2 * bytes);
+        sm100::tma_load_2d_pair(sW(stage, 0), &tw, fl, kb * kBK, wrow);
+        if (SIDES == 2) sm100::tma_load_2d_pair(sW(stage, 1), &tw3, fl, kb * kBK, wrow);
+        load_rows(sX(stage), tx, fl, kb * kBK, xrow, half);
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok && leader) settle<STAGES>(st->full, stage, phase, min(issued, STAGES));
+    }
+  } else if (warp == 1 || (SIDES == 2 && warp == 2)) {
+    if (lane == 0 && leader && live) {
+      const int side = warp - 1;
+      const uint32_t d_tmem = tmem + (uint32_t)(side * 256);
+      const uint32_t idesc = sm100::idesc_i8_s32(256, t.n);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!wait<false>(&st->full[stage], phase, st, p.err, kErrGemmTimeout | 0x83)) {
+          ok = false;
+          break;
+        }
+        sm100::tc_fence_after();
+        const uint64_t da = sm100::sw128_kmajor_desc(sm100::smem_addr(sW(stage, side)));
+        const uint64_t db = sm100::sw128_kmajor_desc(sm100::smem_addr(sX(stage)));
+#pragma unroll
+        for (int k = 0; k < kBK / kStep; ++k)
+          sm100::umma_i8_pair(d_tmem, da + 2 * k, db + 2 * k, idesc, kb != kb0 || k != 0);
+        sm100::umma_commit_pair_mc(&st->empty[stage], pair_mask);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok) sm100::umma_commit_pair_mc(&st->tfull, pair_mask);
+      sm100::umma_commit_pair_mc(&st->drain[side], (uint16_t)(1u << cta));
+      const uint64_t t0 = global_timer_ns();
+      while (!sm100::mbar_try_wait(&st->drain[side], 0) && global_timer_ns() - t0 < kWaitNs) {
+      }
+    }
+  } else if (warp >= 4 && live) {
+    // the scales of this warp's units, then the pair's sums
+    for (int u = set, k = 0; u < units; u += 4, ++k) {
+      const int j = 16 * u + lane;
+      if (lane < 16) xsc->x[16 * k + lane] = j < t.valid ? p.x_scale[t.row + j] : 0.0f;
+    }
+    wait<true>(&st->tfull, 0, st, p.err, kErrGemmTimeout | 0x84);
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::cluster_sync();  // every pair's MMAs are done with its ring
+  sm100::tc_fence_after();
+  const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
+  // where a sender's unit lies in the ring of the CTA that finishes it
+  auto slot = [&](int u, int sender, int owner, int side) {
+    const int from = sender < owner ? sender : sender - 1;
+    const int mine = (u >> 1) / parts;  // of the owner's chunks
+    return (uint32_t)(((((mine * (parts - 1) + from) * SIDES + side) * 2 + (u & 1)) * 4 + q) * UNIT);
+  };
+  auto fetch = [&](int u, int side, uint32_t (&lo)[8], uint32_t (&hi)[8]) {
+    const uint32_t c = tbase + (uint32_t)(side * 256 + 16 * u);
+    sm100::tmem_ld_16x256b_x2(c, lo);
+    sm100::tmem_ld_16x256b_x2(c + (16u << 16), hi);
+  };
+  if (warp >= 4) {
+    for (int u = set; u < units; u += 4) {
+      const int owner = (u >> 1) % parts;
+      if (owner == part) continue;
+#pragma unroll
+      for (int side = 0; side < SIDES; ++side) {
+        uint32_t lo[8], hi[8];
+        fetch(u, side, lo, hi);
+        sm100::tmem_ld_wait();
+        const uint32_t at = sm100::mapa_shared(sm100::smem_addr(base) + slot(u, part, owner, side),
+                                               2 * owner + rank) + lane * 16;
+        send16(at, lo);
+        send16(at + 512, lo + 4);
+        send16(at + 1024, hi);
+        send16(at + 1536, hi + 4);
+      }
+    }
+  }
+  __syncwarp();
+  sm100::tc_fence_before();
+  sm100::cluster_sync();  // what was sent has arrived
+  sm100::tc_fence_after();
+  if (warp >= 4) {
+    float ws1[4], ws3[4];
+    channel_scales(ws1, p.w_scale, p, t, col0, lane);
+    if (SIDES == 2) channel_scales(ws3, p.w3_scale, p, t, col0, lane);
+    for (int u = set, k = 0; u < units; u += 4, ++k) {
+      if ((u >> 1) % parts != part) continue;
+      uint32_t lo[SIDES][8], hi[SIDES][8];
+#pragma unroll
+      for (int side = 0; side < SIDES; ++side) fetch(u, side, lo[side], hi[side]);
+      sm100::tmem_ld_wait();
+      for (int from = 0; from < parts; ++from) {
+        if (from == part) continue;
+#pragma unroll
+        for (int side = 0; side < SIDES; ++side) {
+          const uint4* r = reinterpret_cast<const uint4*>(base + slot(u, from, part, side)) + lane;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = r[32 * i];
+            uint32_t* d = (i < 2 ? lo[side] : hi[side]) + 4 * (i & 1);
+            d[0] += v.x;
+            d[1] += v.y;
+            d[2] += v.z;
+            d[3] += v.w;
+          }
+        }
+      }
+      const float* xs = xsc->x + 16 * k;
+      if constexpr (sizeof(OUT) == 2) {
+        uint32_t r[2][4];
+        if constexpr (SIDES == 2) finish_gated(r, lo[0], hi[0], lo[1], hi[1], xs, ws1, ws3, lane);
+        else finish<ACT>(r, lo[0], hi[0], xs, ws1, lane);
+        write_rows(staging + (warp - 4), &to, p, t, 16 * u, col0, lane, r);
+      } else {
+        // (few rows: the fragments' rows are written as they lie)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int at = 4 * j + 2 * (k4 & 1) + e, i = 8 * j + 2 * (lane & 3) + e;
+              const int c = col0 + (lane >> 2) + 8 * k4;
+              const float a = (float)(int)(k4 < 2 ? lo[0] : hi[0])[at] * (xs[i] * ws1[k4]);
+              float v;
+              if constexpr (SIDES == 2)
+                v = silu_times<OUT>(a, (float)(int)(k4 < 2 ? lo[1] : hi[1])[at] * (xs[i] * ws3[k4]));
+              else
+                v = activate<ACT>(a);
+              if (16 * u + i < t.valid && c < p.n_out)
+                static_cast<OUT*>(p.out)[(size_t)(t.row + 16 * u + i) * p.n_out + c] = v;
+            }
+      }
+    }
+    if (lane == 0) sm100::bulk_wait_read_all();
+  }
+  sm100::tc_fence_before();
+  __syncthreads();
+  sm100::cluster_sync();
+  if (warp == 1) {
+    sm100::tc_fence_after();
+    sm100::tmem_dealloc_pair(tmem, SIDES * 256);
   }
 }
 
@@ -785,30 +1040,75 @@ constexpr size_t smem_bytes(int ring) {
   return (size_t)ring + kEpiWarps * (sizeof(Staging) + sizeof(Scales)) + sizeof(State) + 1024;
 }
 
-template <class K, class... Args>
-cudaError_t launch_i8(K kern, int pairs, size_t bytes, cudaStream_t s, const Args&... args) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+// Raises the kernel's shared-memory limit, once on each device.
+template <class K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <auto kern, class... Args>
+cudaError_t launch_i8(int pairs, size_t bytes, cudaStream_t s, const Args&... args) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, bytes, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), bytes, s, args...);
 }
 
-template <typename OUT>
-cudaError_t run_gemm(const RowMaps& x, const CUtensorMap& w, const CUtensorMap& w3,
-                     const CUtensorMap& o, int act, const I8Params& p, int pairs,
-                     cudaStream_t s) {
+// `tiles` clusters of 2 * parts CTAs
+template <auto kern, class... Args>
+cudaError_t launch_split(int tiles, int parts, size_t bytes, cudaStream_t s, const Args&... args) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, bytes, done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * parts * tiles);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2 * parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename OUT, int ACT>
+cudaError_t run_act(const RowMaps& x, const CUtensorMap& w, const CUtensorMap& w3,
+                    const CUtensorMap& o, const I8Params& p, int tiles, cudaStream_t s) {
   constexpr size_t stream_bytes = smem_bytes<StreamState>(kStreams * kStagesS * kStageBytesS);
   constexpr size_t up_bytes = smem_bytes<UpState>(kStagesU * kStageBytesU);
-  static_assert(stream_bytes <= 232448 && up_bytes <= 232448, "227 KB of shared memory");
+  constexpr size_t split_bytes = smem_bytes<SplitState>(kSplitRing);
+  static_assert(stream_bytes <= 232448 && up_bytes <= 232448 && split_bytes <= 232448,
+                "227 KB of shared memory");
+  if (p.parts > 1)
+    return launch_split<i8_split_kernel<OUT, ACT>>(tiles, p.parts, split_bytes, s, x, w, w3, o, p);
+  const int pairs = tiles < kBlockSms / 2 ? tiles : kBlockSms / 2;
+  if constexpr (ACT == A_SWIGLU)
+    return launch_i8<i8_swiglu_pair_kernel<OUT>>(pairs, up_bytes, s, x, w, w3, o, p);
+  else
+    return launch_i8<i8_pair_kernel<OUT, ACT>>(pairs, stream_bytes, s, x, w, o, p);
+}
+
+template <typename OUT>
+cudaError_t run_gemm(const RowMaps& x, const CUtensorMap& w, const CUtensorMap& w3,
+                     const CUtensorMap& o, int act, const I8Params& p, int tiles,
+                     cudaStream_t s) {
   switch (act) {
-    case MOE_I8_SWIGLU:
-      return launch_i8(i8_swiglu_pair_kernel<OUT>, pairs, up_bytes, s, x, w, w3, o, p);
-    case MOE_I8_RELU:
-      return launch_i8(i8_pair_kernel<OUT, A_RELU>, pairs, stream_bytes, s, x, w, o, p);
-    case MOE_I8_GELU:
-      return launch_i8(i8_pair_kernel<OUT, A_GELU>, pairs, stream_bytes, s, x, w, o, p);
-    default:
-      return launch_i8(i8_pair_kernel<OUT, A_NONE>, pairs, stream_bytes, s, x, w, o, p);
+    case MOE_I8_SWIGLU: return run_act<OUT, A_SWIGLU>(x, w, w3, o, p, tiles, s);
+    case MOE_I8_RELU: return run_act<OUT, A_RELU>(x, w, w3, o, p, tiles, s);
+    case MOE_I8_GELU: return run_act<OUT, A_GELU>(x, w, w3, o, p, tiles, s);
+    default: return run_act<OUT, A_NONE>(x, w, w3, o, p, tiles, s);
   }
 }
 
@@ -862,7 +1162,7 @@ moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq, const fl
     return MOE_ERR_INVALID_ARG;
   RowMaps x;
   for (int b = 0; b < kBoxes; ++b)
-    if (!byte_map(&x.m[b], xq, cfg->rows, cfg->k, 16 << b)) return MOE_ERR_CUDA;
+    if (!byte_map(&x.m[b], xq, cfg->rows, cfg->k, b ? 64 : 16)) return MOE_ERR_CUDA;
   CUtensorMap mw, mw3;
   const long long wrows = (long long)cfg->groups * cfg->n_out;
   if (!byte_map(&mw, w, wrows, cfg->k, 128)) return MOE_ERR_CUDA;
@@ -884,13 +1184,16 @@ moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq, const fl
   p.mt_tiles = (cfg->n_out + 255) / 256;
   p.out = out;
   p.err = static_cast<int*>(ws);
-  // one pair for each two SMs, or one for each tile where there are fewer
-  const long long most = ((long long)cfg->rows / kMaxTok + cfg->groups) * p.mt_tiles;
-  const int pairs = (int)(most < kBlockSms / 2 ? most : kBlockSms / 2);
+  // A bound on the tiles. Few of them leave most SMs idle: K is then split, over
+  // as many pairs as the machine has for each (clusters of 8 and of 4 CTAs do
+  // not fill every GPC, so not quite up to 74 pairs), two K blocks each at least.
+  const long long tiles = ((long long)cfg->rows / kMaxTok + cfg->groups) * p.mt_tiles;
+  const int kblocks = (cfg->k + kBK - 1) / kBK;
+  p.parts = tiles <= 16 && kblocks >= 8 ? 4 : tiles <= 32 && kblocks >= 4 ? 2 : 1;
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = cfg->dtype == MOE_BF16
-                            ? run_gemm<__nv_bfloat16>(x, mw, mw3, mo, cfg->act, p, pairs, s)
-                            : run_gemm<float>(x, mw, mw3, mo, cfg->act, p, pairs, s);
+                            ? run_gemm<__nv_bfloat16>(x, mw, mw3, mo, cfg->act, p, (int)tiles, s)
+                            : run_gemm<float>(x, mw, mw3, mo, cfg->act, p, (int)tiles, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -72,6 +72,25 @@ def test_quantize_borders_and_odd_rows(dtype):
     assert s[0] == 0 and s[4] == 0 and torch.isnan(s[1:3]).all() and not q[:3].any()
 
 
+@pytest.mark.parametrize("exponent", [-90, -3, 0, 11, 100])
+def test_quantize_every_bf16_quotient(exponent):
+    """Every bf16 significand as the row's maximum, with every bf16 value from
+    the maximum down to 2^-10 of it beside it, both signs: the quotients that lie on
+    a border among them."""
+    top = (128 + torch.arange(128, device=DEV, dtype=torch.float64)) * 2.0 ** exponent
+    bits = (128 + torch.arange(128, device=DEV, dtype=torch.float64))[None] * \
+        2.0 ** (exponent - torch.arange(11, device=DEV, dtype=torch.float64))[:, None]
+    x = bits.reshape(1, -1).repeat(128, 1)
+    x = torch.where(x <= top[:, None], x, torch.zeros_like(x))
+    x = torch.cat([top[:, None], x, -x], 1).to(BF)
+    x = torch.cat([x, torch.zeros(128, -x.shape[1] % 8, dtype=BF, device=DEV)], 1)
+    for t in (x, x[:, :-1].contiguous()):
+        q = torch.empty(t.shape, dtype=torch.int8, device=DEV)
+        s = torch.empty(128, device=DEV)
+        block.moe_quantize_rows(t, q, s)
+        check_quantized(t, q, s)
+
+
 def test_quantize_groups_leave_other_rows():
     x = torch.randn((1000, 96), generator=gen(3), device=DEV).to(BF)
     q = torch.full((1000, 96), 77, dtype=torch.int8, device=DEV)
@@ -174,6 +193,24 @@ def test_one_group(rows, k, o, dtype, act):
 ])
 def test_groups(starts, counts, rows, dtype, act):
     c = Gemm(rows, 320, 336, act, dtype, starts, counts, len(starts), seed=rows)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "swiglu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k,o,starts,counts,rows", [
+    (1024, 256, [0], [256], 256),                 # the longest tile, K in four
+    (1040, 272, [0], [193], 193),                 # a K block that ends early
+    (4096, 1024, [3, 40], [37, 230], 270),        # two groups, one of a few rows
+    (2000, 528, [0, 128, 128], [128, 0, 97], 256),  # an empty group
+    (512, 4096, [0], [70], 128),                  # K in two
+    (640, 1936, [0, 100, 250], [100, 150, 33], 283),
+    (1024, 64, [5], [0], 128),                    # no rows at all
+])
+def test_split_reduction(k, o, starts, counts, rows, dtype, act):
+    """Few tiles: K is split over the pairs of a cluster, which join their sums."""
+    c = Gemm(rows, k, o, act, dtype, starts, counts, len(starts), seed=rows + k)
     c.run()
     c.check()
 
