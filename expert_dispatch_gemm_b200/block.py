@@ -67,11 +67,19 @@ class MoeDispatchI8Config(ctypes.Structure):
 
 
 _LIB = None
+_FN = {}  # entry points by name, once loaded
+
+
+def _functions() -> dict:
+    L = lib()
+    _FN.update({s: getattr(L, s) for s in API_SYMBOLS})
+    return _FN
 
 
 def lib() -> ctypes.CDLL:
     global _LIB
     if _LIB is None:
+        _FN.clear()
         if not os.path.exists(LIB_PATH):
             raise RuntimeError(f"{LIB_PATH} is missing: build it with "
                                "`python -m expert_dispatch_gemm_b200.build`")
@@ -116,50 +124,57 @@ def _dtype(dt) -> int:
     return _DTYPES[dt]
 
 
-class _Args:
-    """Checks the tensors of one call and hands out their addresses; they have
-    to be on one CUDA device."""
-    __slots__ = ("device",)
+def _device_of(t) -> int:
+    """The index of the CUDA device that a call's tensors have to be on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    return t.get_device()
 
-    def __init__(self, first):
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise ValueError("expected a CUDA tensor")
-        self.device = first.device
 
-    def __call__(self, t, name, dtype, shape=None, optional=False):
-        if t is None:
-            if optional:
-                return None
-            raise ValueError(f"{name} is missing")
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if t.dtype is not dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.device != self.device:
-            raise ValueError(f"{name} is on {t.device}, not on {self.device}")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _ptr(t, name, dtype, shape, dev):
+    """The address of a tensor of this type, shape and device, or an error that
+    says what is wrong with it. (One pass of cheap tests first: the calls of a
+    decoded token take a few microseconds each.)"""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
         return t.data_ptr()
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
-    def call(self, what, fn, stream, *args):
-        """fn(*args, stream) on the tensors' device; raises MoeError."""
-        index = self.device.index
-        if stream is None:
-            raw = torch._C._cuda_getCurrentRawStream(index)
-        else:
-            if stream.device != self.device:
-                raise ValueError(f"the stream is of {stream.device}, the tensors are on "
-                                 f"{self.device}")
-            raw = stream.cuda_stream
-        if index == torch.cuda.current_device():
+
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _ptr(t, name, dtype, shape, dev)
+
+
+def _ws(ws, dev):
+    return _ptr(ws, "ws", torch.uint8, (ws.numel(),), dev)
+
+
+def _call(what, dev, stream, *args):
+    """The entry point on the tensors' device and stream; raises MoeError."""
+    fn = (_FN or _functions())[what]
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        if stream.device.index != dev:
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on cuda:{dev}")
+        raw = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
             status = fn(*args, raw)
-        else:
-            with torch.cuda.device(index):
-                status = fn(*args, raw)
-        if status != MOE_OK:
-            raise MoeError(status, what)
+    if status != MOE_OK:
+        raise MoeError(status, what)
 
 
 def _check(status: int, what: str):
@@ -171,10 +186,6 @@ def _bytes(device, nbytes: int) -> torch.Tensor:
     ws = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
     off = (-ws.data_ptr()) % 256
     return ws[off:off + nbytes]
-
-
-def _workspace(a: _Args, ws):
-    return a(ws, "ws", torch.uint8), ws.numel()
 
 
 # ---------------------------------------------------------------------------
@@ -204,18 +215,18 @@ def norm_workspace(cfg: MoeNormConfig, device) -> torch.Tensor:
     return _bytes(device, nbytes.value)
 
 
-def _gate(a: _Args, t, name, cfg, dt):
+def _gate(t, name, cfg, dt, n, d, dev):
     """A gate or its gradient: [rows, d] (or [d] for one row) with unit column
     stride and cfg.gate_stride between rows."""
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    rows, d = norm_gate_rows(cfg), cfg.d
+    rows = -(-n // cfg.gate_tokens) if cfg.gate_tokens else 1
     if t.dtype is not dt:
         raise TypeError(f"{name}: expected {dt}, got {t.dtype}")
-    if t.device != a.device:
-        raise ValueError(f"{name} is on {t.device}, not on {a.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{dev}")
     if t.shape != (rows, d) and not (rows == 1 and t.shape == (d,)):
         raise ValueError(f"{name}: expected shape {(rows, d)}, got {tuple(t.shape)}")
     if (d > 1 and t.stride(-1) != 1) or (rows > 1 and t.stride(0) != cfg.gate_stride):
@@ -223,35 +234,40 @@ def _gate(a: _Args, t, name, cfg, dt):
     return t.data_ptr()
 
 
+_F32 = torch.float32
+
+
 def moe_norm_forward(cfg: MoeNormConfig, x, w, h, rstd=None, stream=None):
     """h = norm(x): the pre-norm alone."""
-    a, dt, f32 = _Args(x), _TORCH[cfg.dtype], torch.float32
-    n, d = cfg.n, cfg.d
-    a.call("moe_norm_forward", lib().moe_norm_forward, stream, cfg, a(x, "x", dt, (n, d)),
-           a(w, "w", f32, (d,)), a(h, "h", dt, (n, d)), a(rstd, "rstd", f32, (n,), True))
+    dev, dt, n, d = _device_of(x), _TORCH[cfg.dtype], cfg.n, cfg.d
+    nd = (n, d)
+    _call("moe_norm_forward", dev, stream, cfg, _ptr(x, "x", dt, nd, dev),
+          _ptr(w, "w", _F32, (d,), dev), _ptr(h, "h", dt, nd, dev),
+          _opt(rstd, "rstd", _F32, (n,), dev))
 
 
 def moe_norm_backward(cfg: MoeNormConfig, dres, dh, x, w, rstd, dx, dw, ws, stream=None):
     """dx = dres + d<dh, norm(x)>/dx and dw (dres may be None)."""
-    a, dt, f32 = _Args(x), _TORCH[cfg.dtype], torch.float32
-    nd, n, d = (cfg.n, cfg.d), (cfg.n,), (cfg.d,)
-    a.call("moe_norm_backward", lib().moe_norm_backward, stream, cfg,
-           a(dres, "dres", dt, nd, True), a(dh, "dh", dt, nd), a(x, "x", dt, nd),
-           a(w, "w", f32, d), a(rstd, "rstd", f32, n), a(dx, "dx", dt, nd), a(dw, "dw", f32, d),
-           *_workspace(a, ws))
+    dev, dt, n, d = _device_of(x), _TORCH[cfg.dtype], cfg.n, cfg.d
+    nd = (n, d)
+    _call("moe_norm_backward", dev, stream, cfg, _opt(dres, "dres", dt, nd, dev),
+          _ptr(dh, "dh", dt, nd, dev), _ptr(x, "x", dt, nd, dev), _ptr(w, "w", _F32, (d,), dev),
+          _ptr(rstd, "rstd", _F32, (n,), dev), _ptr(dx, "dx", dt, nd, dev),
+          _ptr(dw, "dw", _F32, (d,), dev), _ws(ws, dev), ws.numel())
 
 
 def moe_residual_norm_forward(cfg: MoeNormConfig, x, y, w_post, gate, w_next, out, h=None,
                               rstd_post=None, rstd_next=None, stream=None):
     """out = res_scale x + block_scale gate * norm(y), h = norm(out); w_post,
     gate, w_next (with h) and the inverse norms may be None."""
-    a, dt, f32 = _Args(x), _TORCH[cfg.dtype], torch.float32
-    nd, n, d = (cfg.n, cfg.d), (cfg.n,), (cfg.d,)
-    a.call("moe_residual_norm_forward", lib().moe_residual_norm_forward, stream, cfg,
-           a(x, "x", dt, nd), a(y, "y", dt, nd), a(w_post, "w_post", f32, d, True),
-           _gate(a, gate, "gate", cfg, dt), a(w_next, "w_next", f32, d, True),
-           a(out, "out", dt, nd), a(h, "h", dt, nd, True),
-           a(rstd_post, "rstd_post", f32, n, True), a(rstd_next, "rstd_next", f32, n, True))
+    dev, dt, n, d = _device_of(x), _TORCH[cfg.dtype], cfg.n, cfg.d
+    nd, n1, d1 = (n, d), (n,), (d,)
+    _call("moe_residual_norm_forward", dev, stream, cfg, _ptr(x, "x", dt, nd, dev),
+          _ptr(y, "y", dt, nd, dev), _opt(w_post, "w_post", _F32, d1, dev),
+          _gate(gate, "gate", cfg, dt, n, d, dev), _opt(w_next, "w_next", _F32, d1, dev),
+          _ptr(out, "out", dt, nd, dev), _opt(h, "h", dt, nd, dev),
+          _opt(rstd_post, "rstd_post", _F32, n1, dev),
+          _opt(rstd_next, "rstd_next", _F32, n1, dev))
 
 
 def moe_residual_norm_backward(cfg: MoeNormConfig, dout, dh, out, y, w_post, gate, w_next,
@@ -259,16 +275,16 @@ def moe_residual_norm_backward(cfg: MoeNormConfig, dout, dh, out, y, w_post, gat
                                stream=None):
     """Gradients of <dout, out> + <dh, h> (see include/moe_block.h for what may
     be None)."""
-    a, dt, f32 = _Args(y), _TORCH[cfg.dtype], torch.float32
-    nd, n, d = (cfg.n, cfg.d), (cfg.n,), (cfg.d,)
-    a.call("moe_residual_norm_backward", lib().moe_residual_norm_backward, stream, cfg,
-           a(dout, "dout", dt, nd, True), a(dh, "dh", dt, nd, True),
-           a(out, "out", dt, nd, True), a(y, "y", dt, nd), a(w_post, "w_post", f32, d, True),
-           _gate(a, gate, "gate", cfg, dt), a(w_next, "w_next", f32, d, True),
-           a(rstd_post, "rstd_post", f32, n, True), a(rstd_next, "rstd_next", f32, n, True),
-           a(dx, "dx", dt, nd), a(dy, "dy", dt, nd), a(dw_post, "dw_post", f32, d, True),
-           _gate(a, dgate, "dgate", cfg, dt), a(dw_next, "dw_next", f32, d, True),
-           *_workspace(a, ws))
+    dev, dt, n, d = _device_of(y), _TORCH[cfg.dtype], cfg.n, cfg.d
+    nd, n1, d1 = (n, d), (n,), (d,)
+    _call("moe_residual_norm_backward", dev, stream, cfg, _opt(dout, "dout", dt, nd, dev),
+          _opt(dh, "dh", dt, nd, dev), _opt(out, "out", dt, nd, dev), _ptr(y, "y", dt, nd, dev),
+          _opt(w_post, "w_post", _F32, d1, dev), _gate(gate, "gate", cfg, dt, n, d, dev),
+          _opt(w_next, "w_next", _F32, d1, dev), _opt(rstd_post, "rstd_post", _F32, n1, dev),
+          _opt(rstd_next, "rstd_next", _F32, n1, dev), _ptr(dx, "dx", dt, nd, dev),
+          _ptr(dy, "dy", dt, nd, dev), _opt(dw_post, "dw_post", _F32, d1, dev),
+          _gate(dgate, "dgate", cfg, dt, n, d, dev), _opt(dw_next, "dw_next", _F32, d1, dev),
+          _ws(ws, dev), ws.numel())
 
 
 # ---------------------------------------------------------------------------
@@ -328,27 +344,25 @@ def grad_workspace(grads: GradList, device) -> torch.Tensor:
     return _bytes(device, nbytes.value)
 
 
-def _grad_args(grads: GradList, norm, ws, least):
-    a = _Args(norm)
-    if grads.device is not None and grads.device != a.device:
-        raise ValueError(f"norm is on {a.device}, the gradients are on {grads.device}")
+def _grad_call(what, grads: GradList, norm, ws, least, stream, *more):
+    dev = _device_of(norm)
+    if grads.device is not None and grads.device.index != dev:
+        raise ValueError(f"norm is on {norm.device}, the gradients are on {grads.device}")
     if norm.numel() < least:
         raise ValueError(f"norm needs {least} elements")
-    return a, a(norm, "norm", torch.float32), *_workspace(a, ws)
+    _call(what, dev, stream, grads.c, grads.count, *more,
+          _ptr(norm, "norm", _F32, norm.shape, dev), _ws(ws, dev), ws.numel())
 
 
 def moe_grad_norm(grads: GradList, norm, ws, stream=None):
     """norm[0] = the L2 norm over all gradients."""
-    a, pn, pw, nw = _grad_args(grads, norm, ws, 1)
-    a.call("moe_grad_norm", lib().moe_grad_norm, stream, grads.c, grads.count, pn, pw, nw)
+    _grad_call("moe_grad_norm", grads, norm, ws, 1, stream)
 
 
 def moe_grad_clip(grads: GradList, max_norm: float, norm, ws, stream=None):
     """norm[0] = the norm, norm[1] = the factor min(1, max_norm / (norm + 1e-6));
     the outputs receive the gradients times the factor."""
-    a, pn, pw, nw = _grad_args(grads, norm, ws, 2)
-    a.call("moe_grad_clip", lib().moe_grad_clip, stream, grads.c, grads.count, max_norm, pn, pw,
-           nw)
+    _grad_call("moe_grad_clip", grads, norm, ws, 2, stream, max_norm)
 
 
 # ---------------------------------------------------------------------------
@@ -379,45 +393,45 @@ def gemm_i8_workspace(cfg: MoeGemmI8Config, device, stream=None) -> torch.Tensor
     return ws
 
 
-def _groups(a: _Args, starts, counts):
+def _groups(starts, counts, dev):
     if (starts is None) != (counts is None):
         raise ValueError("starts and counts come together")
     if starts is None:
         return None, None, 0
     n = starts.numel()
-    return (a(starts, "starts", torch.int32, (n,)), a(counts, "counts", torch.int32, (n,)), n)
+    return (_ptr(starts, "starts", torch.int32, (n,), dev),
+            _ptr(counts, "counts", torch.int32, (n,), dev), n)
 
 
 def moe_quantize_rows(x, q, scale, starts=None, counts=None, stream=None):
     """q, scale = the rows of x [..., cols] in 8 bits with a scale each; with
     starts / counts only the groups' rows are read and written."""
-    a = _Args(x)
-    if x.dim() < 1:
+    dev, shape, dt = _device_of(x), x.shape, x.dtype
+    if not shape:
         raise ValueError("x needs at least one dimension")
-    cols = x.shape[-1]
+    cols = shape[-1]
     rows = x.numel() // cols if cols else 0
-    px, pq = a(x, "x", x.dtype), a(q, "q", torch.int8, x.shape)
-    ps = a(scale, "scale", torch.float32, x.shape[:-1])
-    p0, p1, groups = _groups(a, starts, counts)
-    a.call("moe_quantize_rows", lib().moe_quantize_rows, stream, rows, cols, _dtype(x.dtype), px,
-           pq, ps, p0, p1, groups)
+    p0, p1, groups = _groups(starts, counts, dev)
+    _call("moe_quantize_rows", dev, stream, rows, cols, _dtype(dt), _ptr(x, "x", dt, shape, dev),
+          _ptr(q, "q", torch.int8, shape, dev), _ptr(scale, "scale", _F32, shape[:-1], dev), p0,
+          p1, groups)
 
 
 def moe_gemm_i8(cfg: MoeGemmI8Config, xq, x_scale, starts, counts, w, w_scale, w3, w3_scale, out,
                 ws, stream=None):
     """out = act of the grouped 8-bit products (w3 / w3_scale only for SwiGLU;
     starts and counts None: one group of all rows)."""
-    a, i8, f32 = _Args(xq), torch.int8, torch.float32
+    dev, i8 = _device_of(xq), torch.int8
     g, rows, k, o = cfg.groups, cfg.rows, cfg.k, cfg.n_out
-    p0, p1, n = _groups(a, starts, counts)
+    p0, p1, n = _groups(starts, counts, dev)
     if starts is not None and n != g:
         raise ValueError(f"starts and counts have {n} groups, the config {g}")
     wshape, sshape = (g, o, k), (g, o)
-    a.call("moe_gemm_i8", lib().moe_gemm_i8, stream, cfg, a(xq, "xq", i8, (rows, k)),
-           a(x_scale, "x_scale", f32, (rows,)), p0, p1, a(w, "w", i8, wshape),
-           a(w_scale, "w_scale", f32, sshape), a(w3, "w3", i8, wshape, True),
-           a(w3_scale, "w3_scale", f32, sshape, True), a(out, "out", _TORCH[cfg.dtype], (rows, o)),
-           *_workspace(a, ws))
+    _call("moe_gemm_i8", dev, stream, cfg, _ptr(xq, "xq", i8, (rows, k), dev),
+          _ptr(x_scale, "x_scale", _F32, (rows,), dev), p0, p1, _ptr(w, "w", i8, wshape, dev),
+          _ptr(w_scale, "w_scale", _F32, sshape, dev), _opt(w3, "w3", i8, wshape, dev),
+          _opt(w3_scale, "w3_scale", _F32, sshape, dev),
+          _ptr(out, "out", _TORCH[cfg.dtype], (rows, o), dev), _ws(ws, dev), ws.numel())
 
 
 def dispatch_i8_config(cfg: moe.MoeConfig) -> MoeDispatchI8Config:
@@ -431,15 +445,15 @@ def moe_dispatch_i8(cfg: MoeDispatchI8Config, X, route: RouteBuffers, q, scale, 
                     stream=None):
     """Each token quantised once and written to its dispatched rows (and its
     shared-expert rows); starts / counts = the groups of moe_gemm_i8."""
-    a = _Args(X)
+    dev, i32 = _device_of(X), torch.int32
     g = cfg.E + cfg.n_shared
     for name, shape in (("tok_row", (cfg.n, cfg.slots)), ("offsets", (cfg.E + 1,)),
                         ("counts", (cfg.E,))):
-        a(getattr(route, name), "route." + name, torch.int32, shape)
-    a.call("moe_dispatch_i8", lib().moe_dispatch_i8, stream, cfg,
-           a(X, "X", _TORCH[cfg.dtype], (cfg.n, cfg.d)), ctypes.byref(route.c),
-           a(q, "q", torch.int8, (cfg.rows, cfg.d)), a(scale, "scale", torch.float32, (cfg.rows,)),
-           a(starts, "starts", torch.int32, (g,)), a(counts, "counts", torch.int32, (g,)))
+        _ptr(getattr(route, name), "route." + name, i32, shape, dev)
+    _call("moe_dispatch_i8", dev, stream, cfg, _ptr(X, "X", _TORCH[cfg.dtype], (cfg.n, cfg.d), dev),
+          ctypes.byref(route.c), _ptr(q, "q", torch.int8, (cfg.rows, cfg.d), dev),
+          _ptr(scale, "scale", _F32, (cfg.rows,), dev), _ptr(starts, "starts", i32, (g,), dev),
+          _ptr(counts, "counts", i32, (g,), dev))
 
 
 # ---------------------------------------------------------------------------

@@ -26,6 +26,12 @@ enum : int {
 // measured slower on B200 than letting them start as this one's CTAs exit.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The exception is a kernel of at most one block an SM (the quantisation of a
+// decoded batch): the next kernel's set-up costs more than its blocks' company.
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t s, Args&&... args) {

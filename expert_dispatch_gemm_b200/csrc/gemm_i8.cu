@@ -508,19 +508,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           finish<ACT>(r, lo[b], hi[b], scales_at(xsc, cc), ws, lane);
           write_rows(stg, &to, p, t, cc, col0, lane, r);
         };
-        if (32 * half < t.n) fetch(0, 32 * half);
+        if (32 * half < t.valid) fetch(0, 32 * half);
 #pragma unroll 1
-        for (int cc = 32 * half; cc < t.n; cc += 64) {
+        for (int cc = 32 * half; cc < t.valid; cc += 64) {
           sm100::tmem_ld_wait();
-          fetch(1, cc + 16);
+          const bool more = cc + 16 < t.valid;
+          if (more) fetch(1, cc + 16);
           give(0, cc);
+          if (!more) break;
           sm100::tmem_ld_wait();
-          if (cc + 64 < t.n) fetch(0, cc + 64);
+          if (cc + 64 < t.valid) fetch(0, cc + 64);
           give(1, cc + 16);
         }
       } else {
 #pragma unroll 1
-        for (int cc = 32 * half; cc < t.n; cc += 64) {
+        for (int cc = 32 * half; cc < t.valid; cc += 64) {
           uint32_t v[32];
           sm100::tmem_ld_32x32b_x32(tbase + cc, v);
           sm100::tmem_ld_wait();
@@ -692,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       sm100::tc_fence_after();
       const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
 #pragma unroll 1
-      for (int cc = 32 * half; cc < t.n; cc += 64) {
+      for (int cc = 32 * half; cc + 16 * sub < t.valid; cc += 64) {
         if constexpr (sizeof(OUT) == 2) {
           uint32_t ulo[8], uhi[8], vlo[8], vhi[8], r[2][4];
           const int at = cc + 16 * sub;
@@ -799,6 +801,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     sm100::tmem_alloc_pair(&st->tmem_base, SIDES * 256);
     sm100::tmem_relinquish_pair();
   }
+  const int tile = blockIdx.x / (2 * parts);
+  const int all = (p.K + kBK - 1) / kBK;
+  const int from = all * part / parts, end = all * (part + 1) / parts;
+  // One group and one chunk of rows: the tile's weights are known before the
+  // previous kernel is done, and start on their way to L2 (where what that
+  // kernel may still write to them would arrive too).
+  if (p.groups == 1 && p.rows <= kMaxTok && warp == 3) {
+    for (int kb = from + lane; kb < end; kb += 32) {
+      sm100::tma_prefetch_2d(&tw, kb * kBK, tile * 256 + (int)rank * 128);
+      if (SIDES == 2) sm100::tma_prefetch_2d(&tw3, kb * kBK, tile * 256 + (int)rank * 128);
+    }
+  }
   pdl_wait();
   load_groups(st->g, p, tid);
   sm100::tc_fence_before();
@@ -807,16 +821,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm100::tc_fence_after();
   const uint32_t tmem = st->tmem_base;
 
-  const int tile = blockIdx.x / (2 * parts);
   const bool live = tile < st->g.tiles[p.groups];  // (the same in the whole cluster)
   const Tile t = live ? decode(tile, p, st->g) : Tile{0, 0, 0, 0, 0};
-  const int all = (p.K + kBK - 1) / kBK;
-  const int kb0 = all * part / parts, kb1 = live ? all * (part + 1) / parts : kb0;
+  const int kb0 = from, kb1 = live ? end : from;
   // epilogue warps: quadrant q; units of 16 rows, unit u = 2 chunk + half, by warp set
   const int q = warp & 3, set = (warp - 4) >> 2;
-  const int units = t.n / 16;
+  const int units = (t.valid + 15) / 16;
   const int col0 = t.m0 + (int)rank * 128 + 32 * q;
   Scales* xsc = scales + (warp - 4);
+  float ws1[4], ws3[4];
 
   if (warp == 0) {
     if (lane == 0) {
@@ -882,6 +895,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = 16 * u + lane;
       if (lane < 16) xsc->x[16 * k + lane] = j < t.valid ? p.x_scale[t.row + j] : 0.0f;
     }
+    channel_scales(ws1, p.w_scale, p, t, col0, lane);
+    if (SIDES == 2) channel_scales(ws3, p.w3_scale, p, t, col0, lane);
     wait<true>(&st->tfull, 0, st, p.err, kErrGemmTimeout | 0x84);
   }
   sm100::tc_fence_before();
@@ -891,9 +906,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16);
   // where a sender's unit lies in the ring of the CTA that finishes it
   auto slot = [&](int u, int sender, int owner, int side) {
-    const int from = sender < owner ? sender : sender - 1;
+    const int nth = sender < owner ? sender : sender - 1;
     const int mine = (u >> 1) / parts;  // of the owner's chunks
-    return (uint32_t)(((((mine * (parts - 1) + from) * SIDES + side) * 2 + (u & 1)) * 4 + q) * UNIT);
+    return (uint32_t)(((((mine * (parts - 1) + nth) * SIDES + side) * 2 + (u & 1)) * 4 + q) * UNIT);
   };
   auto fetch = [&](int u, int side, uint32_t (&lo)[8], uint32_t (&hi)[8]) {
     const uint32_t c = tbase + (uint32_t)(side * 256 + 16 * u);
@@ -923,20 +938,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm100::cluster_sync();  // what was sent has arrived
   sm100::tc_fence_after();
   if (warp >= 4) {
-    float ws1[4], ws3[4];
-    channel_scales(ws1, p.w_scale, p, t, col0, lane);
-    if (SIDES == 2) channel_scales(ws3, p.w3_scale, p, t, col0, lane);
     for (int u = set, k = 0; u < units; u += 4, ++k) {
       if ((u >> 1) % parts != part) continue;
       uint32_t lo[SIDES][8], hi[SIDES][8];
 #pragma unroll
       for (int side = 0; side < SIDES; ++side) fetch(u, side, lo[side], hi[side]);
       sm100::tmem_ld_wait();
-      for (int from = 0; from < parts; ++from) {
-        if (from == part) continue;
+      for (int other = 0; other < parts; ++other) {
+        if (other == part) continue;
 #pragma unroll
         for (int side = 0; side < SIDES; ++side) {
-          const uint4* r = reinterpret_cast<const uint4*>(base + slot(u, from, part, side)) + lane;
+          const uint4* r = reinterpret_cast<const uint4*>(base + slot(u, other, part, side)) + lane;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint4 v = r[32 * i];
@@ -1187,7 +1199,8 @@ moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq, const fl
   // A bound on the tiles. Few of them leave most SMs idle: K is then split, over
   // as many pairs as the machine has for each (clusters of 8 and of 4 CTAs do
   // not fill every GPC, so not quite up to 74 pairs), two K blocks each at least.
-  const long long tiles = ((long long)cfg->rows / kMaxTok + cfg->groups) * p.mt_tiles;
+  const long long tiles =
+      ((long long)cfg->rows + (kMaxTok - 1LL) * cfg->groups) / kMaxTok * p.mt_tiles;
   const int kblocks = (cfg->k + kBK - 1) / kBK;
   p.parts = tiles <= 16 && kblocks >= 8 ? 4 : tiles <= 32 && kblocks >= 4 ? 2 : 1;
   cudaStream_t s = (cudaStream_t)stream;

@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : 32 * kQWarps) quantize_kernel(c
   __shared__ long long prefix[MOE_I8_MAX_GROUPS + 1];  // rows of the groups before g
   __shared__ uint32_t red[2][32];
   pdl_wait();
+  if (gridDim.x <= kBlockSms) pdl_trigger();
   const int lane = threadIdx.x & 31;
   long long total = a.rows;
   if (a.starts) {
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(1024) dispatch_i8_kernel(const DispatchI8 a) {
   __shared__ uint32_t red[32];
   __shared__ int dst[MOE_MAX_EXPERTS + MOE_MAX_SHARED];
   pdl_wait();
+  if (gridDim.x <= kBlockSms) pdl_trigger();
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31;
   if (blockIdx.x == 0) {
     for (int g = tid; g < a.E + a.n_shared; g += threads) {
