@@ -5,10 +5,13 @@
 //
 // Two passes over the data, since c needs every element: the floor is one
 // read and one write, and the second read on top of it is kept small by the
-// order. The tensors are cut into tiles of 8,192 elements, each block takes
-// one contiguous run of tiles, and the scaling pass walks the run backwards,
-// so it begins with what the norm pass read last, which the 126 MB L2 still
-// holds. Both passes are bound by HBM.
+// order. Each tensor is cut into equal tiles of up to 8,192 elements; the norm
+// pass deals them out to its blocks in turn, and the scaling pass takes them
+// from the last one backwards, so it begins with what the norm pass read last,
+// which the 126 MB L2 still holds. Both passes are bound by HBM. On a B200, 806 MB
+// of bf16 gradients: 118 us for the norm (the copy rate), 360 us with the clip, where
+// two reads and a write take 369 us at the copy rate; a scaling pass of resident
+// blocks that walk many tiles took 40 us more (its accesses lie further apart).
 //
 // Squares: eight neighbours are summed in fp32 when the largest of them lies
 // in [2^-50, 2^50] (or all are 0), where neither the squares nor their sum
@@ -26,7 +29,7 @@
 namespace moe {
 namespace {
 
-constexpr int kTile = 8192;       // elements
+constexpr int kTile = 8192;       // most elements of a tile
 constexpr int kClipThreads = 256;
 constexpr int kClipBlocks = kBlockSms * 6;  // most blocks of a launch (6 resident on an SM)
 constexpr int kUnroll = 4;        // vectors in flight a thread
@@ -35,9 +38,10 @@ struct GradTensor {
   const void* g;
   void* o;
   long long n;
-  int tile0;  // tiles of the tensors before it (of this launch)
-  int bf16;
+  int tile0;    // tiles of the tensors before it (of this launch)
+  int tile_bf;  // elements of a tile (a multiple of 64), 1 in the low bit for bf16
 };
+__host__ __device__ inline int tile_count(long long n) { return (int)((n + kTile - 1) / kTile); }
 
 // The tensors of one launch travel in its parameters: 4 KB of them hold what
 // one layer has, the largest parameter block (32,764 bytes) what an unstacked
@@ -50,11 +54,6 @@ struct GradBatch {
 constexpr int kSmallBatch = 120, kLargeBatch = 1000;
 static_assert(sizeof(GradBatch<kSmallBatch>) <= 4000, "one 4 KB parameter block");
 static_assert(sizeof(GradBatch<kLargeBatch>) <= 32700, "the largest parameter block");
-
-__device__ __forceinline__ void tile_range(int tiles, int& first, int& last) {
-  first = (int)((long long)blockIdx.x * tiles / gridDim.x);
-  last = (int)((long long)(blockIdx.x + 1) * tiles / gridDim.x);
-}
 
 template <int CAP>
 __device__ __forceinline__ int find_tensor(const GradBatch<CAP>& b, int tile) {
@@ -170,16 +169,13 @@ __global__ void __launch_bounds__(kClipThreads, 6)
     grad_squares_kernel(const __grid_constant__ GradBatch<CAP> b, double* partial) {
   __shared__ double red[kClipThreads / 32];
   pdl_wait();
-  int first, last;
-  tile_range(b.tiles, first, last);
-  int i = find_tensor(b, first);
   double acc = 0.0;
-  for (int tile = first; tile < last; ++tile) {
-    while (i + 1 < b.count && b.t[i + 1].tile0 <= tile) ++i;
-    const GradTensor& t = b.t[i];
-    const long long at = (long long)(tile - t.tile0) * kTile;
-    const int n = (int)min((long long)kTile, t.n - at);
-    acc += t.bf16 ? tile_squares(static_cast<const __nv_bfloat16*>(t.g) + at, n)
+  for (int tile = blockIdx.x; tile < b.tiles; tile += gridDim.x) {
+    const GradTensor& t = b.t[find_tensor(b, tile)];
+    const int size = t.tile_bf & ~1;
+    const long long at = (long long)(tile - t.tile0) * size;
+    const int n = (int)min((long long)size, t.n - at);
+    acc += (t.tile_bf & 1) ? tile_squares(static_cast<const __nv_bfloat16*>(t.g) + at, n)
                   : tile_squares(static_cast<const float*>(t.g) + at, n);
   }
   acc = block_sum(acc, red);
@@ -217,7 +213,7 @@ __device__ __forceinline__ void tile_scale(const T* p, T* o, int n, float c) {
     uint4 r[kUnroll];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k)
-      if (i + k * kClipThreads < vecs) r[k] = __ldcs(q + i + k * kClipThreads);
+      if (i + k * kClipThreads < vecs) r[k] = q[i + k * kClipThreads];
 #pragma unroll
     for (int k = 0; k < kUnroll; ++k) {
       if (i + k * kClipThreads < vecs) {
@@ -225,7 +221,7 @@ __device__ __forceinline__ void tile_scale(const T* p, T* o, int n, float c) {
         Vec16<T>::unpack(r[k], v);
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] *= c;
-        __stcs(w + i + k * kClipThreads, Vec16<T>::pack(v));
+        w[i + k * kClipThreads] = Vec16<T>::pack(v);
       }
     }
   }
@@ -250,18 +246,13 @@ __global__ void __launch_bounds__(kClipThreads, 6)
     norm[0] = (float)r;
     norm[1] = c;
   }
-  if (b.tiles == 0) return;
-  int first, last;
-  tile_range(b.tiles, first, last);
-  int i = find_tensor(b, last - 1);
-  for (int tile = last - 1; tile >= first; --tile) {
-    // (tensors without elements share their successor's tile0)
-    while (b.t[i].tile0 > tile) --i;
-    const GradTensor& t = b.t[i];
+  for (int tile = b.tiles - 1 - (int)blockIdx.x; tile >= 0; tile -= gridDim.x) {
+    const GradTensor& t = b.t[find_tensor(b, tile)];
     if (c == 1.0f && t.g == t.o) continue;
-    const long long at = (long long)(tile - t.tile0) * kTile;
-    const int n = (int)min((long long)kTile, t.n - at);
-    if (t.bf16)
+    const int size = t.tile_bf & ~1;
+    const long long at = (long long)(tile - t.tile0) * size;
+    const int n = (int)min((long long)size, t.n - at);
+    if (t.tile_bf & 1)
       tile_scale(static_cast<const __nv_bfloat16*>(t.g) + at, static_cast<__nv_bfloat16*>(t.o) + at,
                  n, c);
     else
@@ -285,7 +276,7 @@ moe_status check_tensors(const moe_grad_tensor* t, int count, bool outs) {
     if (outs && (!t[i].out || (reinterpret_cast<uintptr_t>(t[i].out) & mask)))
       return MOE_ERR_INVALID_ARG;
     if (t[i].numel > (1LL << 42)) return MOE_ERR_UNSUPPORTED;
-    tiles += (t[i].numel + kTile - 1) / kTile;
+    tiles += tile_count(t[i].numel);
     if (tiles > 0x7fffffff) return MOE_ERR_UNSUPPORTED;
   }
   return MOE_OK;
@@ -303,12 +294,17 @@ void fill(GradBatch<CAP>& b, const moe_grad_tensor* t, int first, int count) {
     g.o = t[i].out;
     g.n = t[i].numel;
     g.tile0 = b.tiles;
-    g.bf16 = t[i].dtype == MOE_BF16;
-    b.tiles += (int)((t[i].numel + kTile - 1) / kTile);
+    const long long tiles = tile_count(g.n);
+    g.tile_bf = (int)(((g.n + tiles - 1) / tiles + 63) / 64 * 64) | (t[i].dtype == MOE_BF16);
+    b.tiles += (int)tiles;
   }
 }
 
 int clip_grid(int tiles) { return tiles < kClipBlocks ? tiles : kClipBlocks; }
+// The scaling pass: a tile a block where there are many (see above); up to a few
+// rounds, which L2 mostly holds, resident blocks save their start (38 MB: 15.7
+// against 17.0 us).
+int scale_grid(int tiles) { return tiles > 4 * kClipBlocks ? tiles : clip_grid(tiles); }
 
 template <int CAP>
 moe_status run_clip(const moe_grad_tensor* t, int count, bool scale, float max_norm, float* norm,
@@ -335,7 +331,7 @@ moe_status run_clip(const moe_grad_tensor* t, int count, bool scale, float max_n
   for (int first = count > 0 ? (count - 1) / CAP * CAP : 0; first >= 0; first -= CAP) {
     fill(b, t, first, count);
     if (b.tiles == 0 && !(write && first == 0)) continue;
-    const int grid = b.tiles ? clip_grid(b.tiles) : 1;
+    const int grid = b.tiles ? scale_grid(b.tiles) : 1;
     if (launch_pdl(grad_scale_kernel<CAP>, dim3(grid), dim3(kClipThreads), 0, s, b,
                    (const double*)partial, used, max_norm, norm, write) != cudaSuccess)
       return MOE_ERR_CUDA;
