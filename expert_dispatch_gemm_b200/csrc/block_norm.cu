@@ -230,6 +230,14 @@ __host__ __device__ __forceinline__ int row_worker(int r, int n, int workers) {
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
+// Gate rows of few tokens travel through the forward's ring with the others (one
+// copy for each row, from L2 after the first; 53.7 against 56.7 us at n 16384, d
+// 2048, 3 tokens a gate row); rows of more tokens are loaded when they begin.
+constexpr int kStagedGateTokens = 8;
+__host__ __device__ __forceinline__ bool gate_staged(const void* gate, int tokens) {
+  return gate && tokens > 0 && tokens <= kStagedGateTokens;
+}
+
 struct NormFwd {
   const void *x, *y, *gate;
   const float *w_post, *w_next;
@@ -275,13 +283,14 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p) {
   T* h = static_cast<T*>(p.h) + base;
   const T* gate = static_cast<const T*>(p.gate);
   if (gate && p.gate_tokens) gate += (long long)(r0 / p.gate_tokens) * p.gate_stride;
-  const bool gate_each = gate && p.gate_tokens == 1;  // its rows travel with the others
+  const bool gate_each = gate_staged(gate, p.gate_tokens);
   const uint32_t pitch = (uint32_t)blockDim.x * EPT * sizeof(T);  // of a staged row
   Ring ring(nsm, p.slots * pitch, p.stages);
   const float inv_d = 1.0f / (float)p.d;
   size_t fill_at = 0;
   const T* fill_gate = gate;
   int to_fill = r1 - r0;
+  int fill_left = gate_each ? p.gate_tokens - r0 % p.gate_tokens : 0;
   auto issue = [&]() {
     if constexpr (STAGED) {
       if (to_fill > 0) {
@@ -297,7 +306,10 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p) {
           if (gate_each) cp_async<B>(dst + 2 * pitch, fill_gate + c, n);
         }
         fill_at += p.d;
-        fill_gate += p.gate_stride;
+        if (gate_each && --fill_left == 0) {
+          fill_gate += p.gate_stride;
+          fill_left = p.gate_tokens;
+        }
         ring.filled();
       }
       cp_async_commit();
@@ -404,7 +416,7 @@ cudaError_t launch_fwd(NormFwd& p, int bytes, cudaStream_t s) {
   const int per_sm = fwd_workers_per_sm(p.d);
   const long long most = (long long)kBlockSms * per_sm;
   p.workers = (int)(p.n < most ? p.n : most);
-  p.slots = p.gate && p.gate_tokens == 1 ? 3 : p.y ? 2 : 1;
+  p.slots = gate_staged(p.gate, p.gate_tokens) ? 3 : p.y ? 2 : 1;
   const size_t row = (size_t)norm_threads(p.d) * (p.d > 8192 ? 16 : 8) * sizeof(T);
   const size_t fit = ring_budget(per_sm) / (p.slots * row);
   const int deep = (p.n + p.workers - 1) / p.workers;  // no more stages than rows
@@ -480,16 +492,20 @@ __device__ __forceinline__ void worker_sum3(float& a, float& b, float& c, float4
 // Sums over tokens: dw_next in registers over all of the worker's rows; the
 // gate's and dw_post share one, A = sum D yr over the rows of one gate row,
 // of which they are dgate = b (w_post + off) A and dw_post += b gate A, taken
-// when the gate row or the range ends (dw_post's running sum waits in shared
-// memory between).
+// when the gate row or the range ends (where rows of several gates meet in a
+// range, dw_post's running sum waits in shared memory between). With 64
+// registers a thread the next norm's weights are read from shared memory, not
+// kept: what the compiler spilled instead missed the small L1 that the rings
+// leave (182 against 151 us at n 8192, d 7168, 1,024 tokens a gate row).
 template <typename T, int VEC, int EPT, bool STAGED, int MAXT, bool ALL>
 __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
   extern __shared__ __align__(16) unsigned char nsm[];
   __shared__ float4 red[2][32];
   pdl_wait();
   constexpr int P = EPT / 2;
-  // with 64 registers a thread, y is read again for the second half of a row
-  constexpr bool KEEP_Y = MAXT <= 768;
+  // with 64 registers a thread, y is read again for the second half of a row,
+  // and the next norm's weights for each row
+  constexpr int KEEP = MAXT <= 768;
   const Cols<T, VEC, EPT> cols{(int)threadIdx.x, (int)blockDim.x, p.d / VEC};
   const int warps = blockDim.x >> 5;
   const int group = threadIdx.y, groups = blockDim.y;
@@ -505,16 +521,23 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
   auto in = [](const void* q, size_t at) { return static_cast<const T*>(q) + at; };
   auto to = [](void* q, size_t at) { return static_cast<T*>(q) + at; };
   const float inv_d = 1.0f / (float)p.d;
-  // the workers' rings; each takes the sums of dw_next and of the one gate row
-  // at its worker's end; then the running sums of dw_post (fp32, [columns] each)
+  // the workers' rings; each takes its worker's sums of dw_next, of the one gate
+  // row and of dw_post at the end; then, [columns] of fp32 a worker each, the
+  // running sums of dw_post and the next norm's weights
   const uint32_t pitch = (uint32_t)blockDim.x * EPT * sizeof(T);
   const uint32_t fpitch = (uint32_t)blockDim.x * EPT;
   unsigned char* mine = nsm + (size_t)group * p.ring_bytes;
   Ring ring(mine, p.slots * pitch, p.stages);
-  float* end_next = reinterpret_cast<float*>(mine);
-  float* end_gate = end_next + (next ? fpitch : 0);
-  float* sum_post =
-      reinterpret_cast<float*>(nsm + (size_t)groups * p.ring_bytes) + (size_t)group * fpitch;
+  const bool running = post && p.gate && p.gate_tokens;
+  // (addresses of what is used seldom are made where it is)
+  auto ring_end = [&](int which) {
+    return reinterpret_cast<float*>(nsm + (size_t)group * p.ring_bytes) + which * fpitch;
+  };
+  auto extra = [&](int which) {
+    return reinterpret_cast<float*>(nsm + (size_t)groups * p.ring_bytes) +
+           (size_t)(which * groups + group) * fpitch;
+  };
+  const int at_gate = next ? 1 : 0, at_post = at_gate + (gate_all ? 1 : 0);
   // offsets of a stage's rows, in this order where present: dh, out, y, dout, gate
   const uint32_t s_y = next ? 2 * pitch : 0, s_dout = s_y + (has_y ? pitch : 0),
                  s_gate = s_dout + (has_dout ? pitch : 0);
@@ -550,7 +573,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
 #pragma unroll
     for (int e = 0; e < P; ++e) wn[e] = add2(wn[e], both(p.off));
   }
-  if (post) cols.store_f32(sum_post, A);
+  if (!KEEP && EPT == 8 && next) cols.store_f32(extra(running ? 1 : 0), wn);
+  if (running) cols.store_f32(extra(0), A);
   // w_post + off (1 without)
   auto post_weights = [&](float2* v) {
     if (post) {
@@ -605,6 +629,15 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
       if (STAGED) cols.load_smem(u, ring.read + pitch), cols.load_smem(v, ring.read);
       else cols.load(u, in(p.out, at)), cols.load(v, in(p.dh, at));
       float2 s1 = both(0.0f);
+      if constexpr (!KEEP) {
+        if constexpr (EPT == 8) {
+          cols.load_f32(wn, extra(running ? 1 : 0));
+        } else {  // (shared memory is short here)
+          cols.load_f32(wn, p.w_next);
+#pragma unroll
+          for (int e = 0; e < P; ++e) wn[e] = add2(wn[e], both(p.off));
+        }
+      }
 #pragma unroll
       for (int e = 0; e < P; ++e) {
         u[e] = mul2(u[e], both(rn));
@@ -638,7 +671,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
       worker_sum3(k1, a2, a3, red[r & 1] + group * warps, warps);
       k1 *= rn * inv_d;                            // r2 mean(q u)
       k2 = rp * rp * rp * (a2 - k1 * a3) * inv_d;  // r1^2 mean(D c); 0 without the norm
-      if (has_y && !KEEP_Y) load_y();
+      if (has_y && !KEEP) load_y();
     }
 #pragma unroll
     for (int e = 0; e < P; ++e) {
@@ -670,7 +703,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
           const long long first = (long long)gi * p.gate_tokens;
           const long long last = p.gate_tokens ? min(first + p.gate_tokens, (long long)p.n) : p.n;
           if (gate_all)
-            cols.store_f32(end_gate, wp);
+            cols.store_f32(ring_end(at_gate), wp);
           else if (first < r0)
             cols.store_f32(p.part_head + (size_t)w * p.pitch, wp);
           else if (last > r1)
@@ -678,11 +711,15 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
           else
             cols.store(static_cast<T*>(p.dgate) + (long long)gi * p.gate_stride, wp);
         }
-        if (post) {
-          cols.load_f32(wp, sum_post);
+        if (running) {
+          cols.load_f32(wp, extra(0));
 #pragma unroll
           for (int e = 0; e < P; ++e) wp[e] = fma2(g[e], A[e], wp[e]);
-          cols.store_f32(sum_post, wp);
+          cols.store_f32(extra(0), wp);
+        } else if (post) {  // (the range's end: the ring is done with)
+#pragma unroll
+          for (int e = 0; e < P; ++e) wp[e] = mul2(g[e], A[e]);
+          cols.store_f32(ring_end(at_post), wp);
         }
 #pragma unroll
         for (int e = 0; e < P; ++e) A[e] = both(0.0f);
@@ -690,21 +727,25 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
     }
     ring.done();
   }
-  if (next) cols.store_f32(end_next, acc_n);
-  if (gate_all && r0 == r1) cols.store_f32(end_gate, A);
+  if (next) cols.store_f32(ring_end(0), acc_n);
+  if (r0 == r1) {  // no rows: A is zeros
+    if (gate_all) cols.store_f32(ring_end(at_gate), A);
+    if (post && !running) cols.store_f32(ring_end(at_post), A);
+  }
   __syncthreads();
   // the workers' sums, in their order
   const bool alone = p.blocks == 1;
   const size_t ring_f = p.ring_bytes / 4;
   const float* ends = reinterpret_cast<const float*>(nsm);
-  const float* posts = reinterpret_cast<const float*>(nsm + (size_t)groups * p.ring_bytes);
+  const float* sums = reinterpret_cast<const float*>(nsm + (size_t)groups * p.ring_bytes);
   const size_t row = alone ? 0 : (size_t)blockIdx.x * p.pitch;
   for (int c = group * blockDim.x + threadIdx.x; c < p.d; c += groups * blockDim.x) {
     float a = 0.0f, b = 0.0f, g = 0.0f;
     for (int k = 0; k < groups; ++k) {
-      if (post) a += posts[(size_t)k * fpitch + c];
+      if (running) a += sums[(size_t)k * fpitch + c];
+      else if (post) a += ends[k * ring_f + at_post * fpitch + c];
       if (next) b += ends[k * ring_f + c];
-      if (gate_all) g += ends[k * ring_f + (next ? fpitch : 0) + c];
+      if (gate_all) g += ends[k * ring_f + at_gate * fpitch + c];
     }
     if (post) (alone ? p.dw_post : p.part_post + row)[c] = a;
     if (next) (alone ? p.dw_next : p.part_next + row)[c] = b;
@@ -718,10 +759,13 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
 // Joins the partial sums in order: 128 columns a block, 32 slices of the
 // partial rows, then the slices. blockIdx.y: dw_post, dw_next, then the gate: its
 // one row, or the rows that more than one worker holds, found by row (fewer
-// rows than workers) or by the worker that they begin in.
+// rows than workers) or by the worker that they begin in. Rows that span a few
+// workers only are a slice's work each, 32 to a block (at n 16384, d 2048, 3 tokens
+// a gate row, a block each took 95 us).
 struct NormReduce {
   NormBwd b;
   int by_group;
+  int slice_rows;  // a gate row a slice
 };
 constexpr int kRedSlices = 32;
 
@@ -735,6 +779,8 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
   const float* src;        // the others': src + w * pitch
   int w_lo = 0, w_hi = p.blocks;  // partial rows w_lo .. w_hi - 1
   long long group = 0;
+  bool mine = true;  // (with a slice a row, a slice may have none)
+  const bool slices = job >= 2 && q.slice_rows;
   if (job == 0) {
     if (!p.w_post) return;
     first_src = src = p.part_post;
@@ -745,26 +791,32 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
     first_src = src = p.part_gate;
   } else {
     const long long tokens = p.gate_tokens;
-    if (q.by_group) {
-      group = job - 2;
-    } else {
-      const int end = worker_row(job - 2 + 1, p.n, p.workers);
-      if (end == worker_row(job - 2, p.n, p.workers)) return;
-      group = (end - 1) / tokens;
+    const long long rows = (p.n + tokens - 1) / tokens;
+    const long long nth = slices ? (long long)(job - 2) * kRedSlices + threadIdx.y : job - 2;
+    mine = nth < (q.by_group ? rows : p.workers);
+    if (mine) {
+      if (q.by_group) {
+        group = nth;
+      } else {
+        const int end = worker_row((int)nth + 1, p.n, p.workers);
+        mine = end != worker_row((int)nth, p.n, p.workers);
+        group = (end - 1) / tokens;
+      }
+      const long long first = group * tokens, last = min(first + tokens, (long long)p.n);
+      w_lo = row_worker((int)first, p.n, p.workers);
+      w_hi = row_worker((int)last - 1, p.n, p.workers) + 1;
+      if (!q.by_group && w_lo != nth) mine = false;  // it began earlier
+      if (w_hi - w_lo == 1) mine = false;            // one worker holds it: already written
     }
-    const long long first = group * tokens, last = min(first + tokens, (long long)p.n);
-    w_lo = row_worker((int)first, p.n, p.workers);
-    w_hi = row_worker((int)last - 1, p.n, p.workers) + 1;
-    if (!q.by_group && w_lo != job - 2) return;  // it began earlier
-    if (w_hi - w_lo == 1) return;                // one worker holds it: already written
+    if (!slices && !mine) return;
     src = p.part_head;
     first_src = p.part_tail + (size_t)w_lo * p.pitch;
   }
   const int col = (blockIdx.x * 32 + threadIdx.x) * 4;
   float4 s = make_float4(0, 0, 0, 0);
-  if (col < p.pitch) {
+  if (col < p.pitch && mine) {
 #pragma unroll 4
-    for (int w = w_lo + threadIdx.y; w < w_hi; w += kRedSlices) {
+    for (int w = w_lo + (slices ? 0 : threadIdx.y); w < w_hi; w += slices ? 1 : kRedSlices) {
       const float* row = w == w_lo ? first_src : src + (size_t)w * p.pitch;
       const float4 v = *reinterpret_cast<const float4*>(row + col);
       s.x += v.x;
@@ -772,6 +824,19 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
       s.z += v.z;
       s.w += v.w;
     }
+  }
+  auto put = [&](const float4& r) {
+    const float v[4] = {r.x, r.y, r.z, r.w};
+    for (int j = 0; j < 4; ++j) {
+      if (col + j >= p.d) break;
+      if (job == 0) p.dw_post[col + j] = v[j];
+      else if (job == 1) p.dw_next[col + j] = v[j];
+      else static_cast<T*>(p.dgate)[group * p.gate_stride + col + j] = T(v[j]);
+    }
+  };
+  if (slices) {
+    if (mine) put(s);
+    return;
   }
   part[threadIdx.y][threadIdx.x] = s;
   __syncthreads();
@@ -783,13 +848,7 @@ __global__ void __launch_bounds__(32 * kRedSlices) norm_reduce_kernel(const Norm
     s.z += v.z;
     s.w += v.w;
   }
-  const float v[4] = {s.x, s.y, s.z, s.w};
-  for (int j = 0; j < 4; ++j) {
-    if (col + j >= p.d) break;
-    if (job == 0) p.dw_post[col + j] = v[j];
-    else if (job == 1) p.dw_next[col + j] = v[j];
-    else static_cast<T*>(p.dgate)[group * p.gate_stride + col + j] = T(v[j]);
-  }
+  put(s);
 }
 
 // ---- work split of the backward ---------------------------------------------
@@ -836,8 +895,12 @@ cudaError_t launch_bwd(NormBwd& p, int groups, int bytes, cudaStream_t s) {
   constexpr int V16 = 16 / sizeof(T), V4 = 4 / sizeof(T);
   const size_t cols = (size_t)norm_threads(p.d) * (p.d > 8192 ? 16 : 8);
   const size_t row = cols * sizeof(T);
-  const size_t sums = p.w_post ? cols * 4 : 0;
-  const size_t ends = cols * 4 * ((p.w_next ? 1 : 0) + (p.gate && p.gate_tokens == 0 ? 1 : 0));
+  const bool gate_all = p.gate && p.gate_tokens == 0;
+  const bool running = p.w_post && p.gate && p.gate_tokens;
+  const bool few = norm_threads(p.d) <= 256 && bytes >= 4;  // 80 registers a thread, not 64
+  const size_t sums = cols * 4 * ((running ? 1 : 0) + (p.w_next && !few && p.d <= 8192 ? 1 : 0));
+  const size_t ends =
+      cols * 4 * ((p.w_next ? 1 : 0) + (gate_all ? 1 : 0) + (p.w_post && !running ? 1 : 0));
   p.slots = (p.dh ? 2 : 0) + (p.y ? 1 : 0) + (p.dout ? 1 : 0) +
             (p.gate && p.gate_tokens == 1 ? 1 : 0);
   const size_t budget = ring_budget(groups);
@@ -853,7 +916,6 @@ cudaError_t launch_bwd(NormBwd& p, int groups, int bytes, cudaStream_t s) {
   if (!staged)
     return p.d > 8192 ? run_bwd<T, 1, 16, false, 1024>(p, groups, smem, s)
                       : run_bwd<T, 1, 8, false, 1024>(p, groups, smem, s);
-  const bool few = norm_threads(p.d) <= 256;
   if (bytes < 16) {
     if (p.d > 8192) return run_bwd<T, V4, 16, true, 1024>(p, groups, smem, s);
     return few ? run_bwd<T, V4, 8, true, 768>(p, groups, smem, s)
@@ -980,13 +1042,15 @@ moe_status backward_impl(const moe_norm_config* c, const NormBwd& q, void* ws, s
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   const bool shared_rows = p.gate && p.gate_tokens > 1;  // gate rows of several workers
   if (p.blocks == 1 && (!shared_rows || p.workers == 1)) return MOE_OK;
-  NormReduce r{p, 0};
+  NormReduce r{p, 0, 0};
   if (p.blocks == 1) r.b.w_post = r.b.w_next = nullptr;  // (written already)
   int jobs = 2;
   if (shared_rows) {
     const int rows = gate_rows(c);
     r.by_group = rows <= p.workers;
-    jobs += r.by_group ? rows : p.workers;
+    const int each = r.by_group ? rows : p.workers;
+    r.slice_rows = (long long)p.gate_tokens * p.workers <= 4LL * p.n;
+    jobs += r.slice_rows ? (each + kRedSlices - 1) / kRedSlices : each;
   } else if (p.gate && p.gate_tokens == 0) {
     ++jobs;
   }
