@@ -156,6 +156,8 @@ def _opt(t, name, dtype, shape, dev):
 
 
 def _ws(ws, dev):
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws: expected a torch.Tensor")
     return _ptr(ws, "ws", torch.uint8, (ws.numel(),), dev)
 
 
@@ -293,7 +295,8 @@ def moe_residual_norm_backward(cfg: MoeNormConfig, dout, dh, out, y, w_post, gat
 
 class GradList:
     """The gradients of one moe_grad_norm / moe_grad_clip call, and where the
-    clipped copies go (None: in place). Holds the tensors."""
+    clipped copies go (None: in place). Holds the tensors; their addresses are
+    taken here, once."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -482,6 +485,12 @@ class QuantizedLayer:
     def __init__(self, w: Workload, inputs: dict, device, **cfg_override):
         self.w = w
         self.cfg = cfg = moe.config(w, **cfg_override)
+        sz, dt, g = moe.sizes(cfg), w.torch_dtype, cfg.E + cfg.n_shared
+        self.dispatch_cfg = dispatch_i8_config(cfg)
+        self.up = gemm_i8_config(g, sz.rows, cfg.d, cfg.h, w.act, dt)
+        self.down = gemm_i8_config(g, sz.rows, cfg.h, cfg.d, "none", dt)
+        for c in (self.up, self.down):  # (d and h have to be multiples of 16)
+            _check(gemm_i8_validate(c), "moe_gemm_i8_validate")
         self.Wg, self.logit_bias = inputs["Wg"], inputs.get("logit_bias")
         self.sel_bias = inputs.get("sel_bias")
         self.W1, self.s1 = quantize_weights(inputs["W1"], inputs.get("sW1"))
@@ -490,10 +499,6 @@ class QuantizedLayer:
                             if w.act == "swiglu" else (None, None))
         self.route = RouteBuffers(cfg, device)
         self.ws = moe.workspace(cfg, device, layer=False)
-        sz, dt, g = self.route.sizes, w.torch_dtype, cfg.E + cfg.n_shared
-        self.dispatch_cfg = dispatch_i8_config(cfg)
-        self.up = gemm_i8_config(g, sz.rows, cfg.d, cfg.h, w.act, dt)
-        self.down = gemm_i8_config(g, sz.rows, cfg.h, cfg.d, "none", dt)
         f32, i32, i8 = torch.float32, torch.int32, torch.int8
         self.Xq = torch.empty((sz.rows, cfg.d), dtype=i8, device=device)
         self.xs = torch.empty(sz.rows, dtype=f32, device=device)
@@ -563,6 +568,8 @@ class Block:
     def grads(self):
         """Gradient buffers (allocated once): "dx", the norms' and the gate's,
         and the layer's own."""
+        if not hasattr(self.layer, "backward_train"):
+            raise TypeError(f"a {type(self.layer).__name__} has no backward pass")
         if self._g is None:
             p, g = self.p, {"dx": torch.empty_like(self.out), "dy": torch.empty_like(self.out),
                             "dw_pre": torch.empty_like(self.p["w_pre"])}

@@ -57,6 +57,13 @@ static_assert(sizeof(GradBatch<kLargeBatch>) <= 32700, "the largest parameter bl
 
 template <int CAP>
 __device__ __forceinline__ int find_tensor(const GradBatch<CAP>& b, int tile) {
+  if (CAP == kLargeBatch) {
+    // long lists are mostly of like tensors, found at once (768 of 25 k elements:
+    // 21.5 against 25.5 us a clip)
+    const int i = (int)((float)tile * b.count / b.tiles);
+    if (i < b.count && b.t[i].tile0 <= tile && (i + 1 == b.count || b.t[i + 1].tile0 > tile))
+      return i;
+  }
   int lo = 0, hi = b.count - 1;  // the last tensor with tile0 <= tile (empty ones have no tile)
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;

@@ -1,6 +1,9 @@
 """A block (pre-norm, layer, post-norm with gate and residual, next pre-norm)
 run as a user runs it: serving, training with the clip, and in a graph."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -160,3 +163,126 @@ def test_decode_step_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     del graph
+
+
+CHECKED = os.environ.get("MOE_LIBRARY") == "checked"
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _run(args, **env):
+    r = subprocess.run([sys.executable, *args], env=dict(os.environ, **env), cwd=ROOT,
+                       capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, (r.stdout + r.stderr)[-3000:]
+    return r.stdout
+
+
+@pytest.mark.skipif(CHECKED, reason="the driver of the checked run")
+def test_checked_build():
+    """The same products and layers in the checked build, where every group that
+    does not fit its buffers is reported; the test below plants one."""
+    out = _run(["-m", "pytest", "-q", "-m", "gpu", "-p", "no:cacheprovider",
+                "tests/test_gpu_i8.py", "tests/test_gpu_block.py", "-k",
+                "one_group or many_groups or split_reduction or quantized_layer or train_step "
+                "or serving or reports_groups"], MOE_LIBRARY="checked")
+    assert " passed" in out and "failed" not in out
+
+
+@pytest.mark.skipif(not CHECKED, reason="runs under the checked build (MOE_LIBRARY=checked)")
+def test_checked_build_reports_groups_that_do_not_fit():
+    cfg = block.gemm_i8_config(2, 64, 32, 16)
+    i8 = dict(dtype=torch.int8, device=DEV)
+    x, w = torch.ones((64, 32), **i8), torch.ones((2, 16, 32), **i8)
+    xs, s = torch.ones(64, device=DEV), torch.ones((2, 16), device=DEV)
+    out = torch.zeros((64, 16), dtype=torch.bfloat16, device=DEV)
+    ws = block.gemm_i8_workspace(cfg, DEV)
+    at = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    for counts, code in (([40, 24], 0), ([40, 30], 0x221)):
+        n = torch.tensor(counts, dtype=torch.int32, device=DEV)
+        block.moe_gemm_i8(cfg, x, xs, at, n, w, s, None, None, out, ws)
+        torch.cuda.synchronize()
+        assert moe.moe_read_error(ws)[1] == code
+        assert bool((out == 32.0).all())  # cut to the rows that are there
+
+
+FIRST_CALLS = """
+import torch
+from expert_dispatch_gemm_b200 import block
+dev, bf = "cuda", torch.bfloat16
+n, d, o = 40, 256, 256
+x = torch.randn(n, d, device=dev).to(bf)
+y, dout, dh = x * 2, x.clone(), x.clone()
+w = torch.ones(d, device=dev)
+out, h, dx, dy = (torch.empty_like(x) for _ in range(4))
+r1, r2 = torch.empty(n, device=dev), torch.empty(n, device=dev)
+dw1, dw2 = torch.empty(d, device=dev), torch.empty(d, device=dev)
+cfg = block.norm_config(n, d, bf, 1e-6)
+ws = block.norm_workspace(cfg, dev)
+g = [torch.ones(1000, device=dev), torch.ones(333, device=dev, dtype=bf)]
+glist = block.grad_list(g)
+gws, norm = block.grad_workspace(glist, dev), torch.empty(2, device=dev)
+q, qs = torch.empty((n, d), dtype=torch.int8, device=dev), torch.empty(n, device=dev)
+wq = torch.ones((1, o, d), dtype=torch.int8, device=dev)
+wsc = torch.ones((1, o), device=dev)
+c = block.gemm_i8_config(1, n, d, o)
+prod, iws = torch.empty((n, o), device=dev, dtype=bf), block.gemm_i8_workspace(c, dev)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    block.moe_residual_norm_forward(cfg, x, y, w, None, w, out, h, r1, r2)
+    block.moe_residual_norm_backward(cfg, dout, dh, out, y, w, None, w, r1, r2, dx, dy, dw1, None,
+                                     dw2, ws)
+    block.moe_grad_clip(glist, 1.0, norm, gws)
+    block.moe_quantize_rows(h, q, qs)
+    block.moe_gemm_i8(c, q, qs, None, None, wq, wsc, None, None, prod, iws)
+graph.replay()
+torch.cuda.synchronize()
+ref = (q.double().sum(1) * qs.double())[:, None].expand(n, o)
+assert ((prod.double() - ref).abs() <= 2 ** -8 * ref.abs() + 1e-30).all()
+assert abs(norm[0].item() - 1333 ** 0.5) < 1e-4
+assert torch.isfinite(dx).all() and torch.isfinite(dw1).all()
+print("replayed")
+"""
+
+
+@pytest.mark.skipif(CHECKED, reason="once is enough")
+def test_first_calls_of_a_process_inside_a_capture():
+    assert "replayed" in _run(["-c", FIRST_CALLS])
+
+
+def test_wrong_use_is_refused():
+    w = wl.SMALL[3]
+    inp = wl.make_inputs(w, DEV)
+    p = {"w_pre": torch.ones(w.d, device=DEV), "w_next": torch.ones(w.d, device=DEV)}
+    fast = block.Block(block.QuantizedLayer(w, inp, DEV), p)
+    with pytest.raises(TypeError):  # 8-bit experts have no backward pass
+        fast.grads()
+    b = block.Block(moe.Layer(w, inp, DEV), p)
+    out, _ = b.forward_train(inp["X"])
+    with pytest.raises(ValueError):  # h_next's gradient is missing
+        b.backward_train(torch.ones_like(out))
+    with pytest.raises(moe.MoeError):  # d is not a multiple of 16
+        v = wl.EC_FP32.replace(d=24, h=40)
+        block.QuantizedLayer(v, wl.make_inputs(v, DEV), DEV)
+    t = torch.ones(100, device=DEV)
+    with pytest.raises(ValueError):  # the same tensor twice, in place
+        block.grad_list([t, t])
+    with pytest.raises(ValueError):  # an output over another gradient
+        block.grad_list([t[:50], t[50:]], [t[50:], torch.empty(50, device=DEV)])
+    with pytest.raises(ValueError):
+        block.grad_list([t[::2]])
+    glist = block.grad_list([t, t], [torch.empty_like(t), torch.empty_like(t)])  # read twice: fine
+    norm = torch.empty(2, device=DEV)
+    block.moe_grad_clip(glist, 1.0, norm, block.grad_workspace(glist, DEV))
+    assert abs(norm[0].item() - 200 ** 0.5) < 1e-5
+    with pytest.raises(ValueError):
+        block.moe_grad_clip(glist, 1.0, norm[:1], block.grad_workspace(glist, DEV))
+    cfg = block.norm_config(4, 64, torch.bfloat16, 1e-6, gate_tokens=2)
+    x = torch.ones(4, 64, device=DEV, dtype=torch.bfloat16)
+    o, one = torch.empty_like(x), torch.ones(64, device=DEV)
+    for bad in (x.float(), x[:3], x.t(), x.cpu()):
+        with pytest.raises((ValueError, TypeError)):
+            block.moe_residual_norm_forward(cfg, x, bad, one, None, None, o)
+    with pytest.raises(ValueError):  # two gate rows are wanted
+        block.moe_residual_norm_forward(cfg, x, x, one, x[:1], None, o)
+    with pytest.raises(moe.MoeError):  # w_next without h
+        block.moe_residual_norm_forward(cfg, x, x, one, None, one, o)
