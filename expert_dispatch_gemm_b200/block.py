@@ -131,11 +131,11 @@ def _device_of(t) -> int:
     return t.get_device()
 
 
-def _ptr(t, name, dtype, shape, dev):
+def _ptr(t, name, dtype, shape, dev, _Tensor=torch.Tensor):
     """The address of a tensor of this type, shape and device, or an error that
     says what is wrong with it. (One pass of cheap tests first: the calls of a
     decoded token take a few microseconds each.)"""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape
             and t.get_device() == dev and t.is_contiguous()):
         return t.data_ptr()
     if t is None:

@@ -172,7 +172,7 @@ struct Tile {
 
 // Tile order: group by group, 256 channels by 256, the rows' chunks innermost
 // (pairs that run together share a weight tile). A group's rows are split
-// into ceil(count / 256) chunks of equal size (rounded up to 32).
+// into ceil(count / 256) chunks of 32-row units, equal to a unit.
 __device__ __forceinline__ Tile decode(int tile, const I8Params& p, const GroupTable& g) {
   int lo = 0, hi = p.groups - 1;
   while (lo < hi) {
@@ -184,11 +184,14 @@ __device__ __forceinline__ Tile decode(int tile, const I8Params& p, const GroupT
   const int chunks = max((count + kMaxTok - 1) / kMaxTok, 1);
   const int local = tile - g.tiles[lo];
   const int chunk = local % chunks;
-  const int size = ((count + chunks - 1) / chunks + kTokUnit - 1) / kTokUnit * kTokUnit;
+  const int units = (count + kTokUnit - 1) / kTokUnit;
+  const int each = units / chunks, more = units % chunks;  // the first `more` have one more
+  const int first = (chunk * each + min(chunk, more)) * kTokUnit;
+  const int last = min(first + (each + (chunk < more)) * kTokUnit, count);
   t.group = lo;
   t.m0 = local / chunks * 256;
-  t.row = g.start[lo] + chunk * size;
-  t.valid = min(size, count - chunk * size);
+  t.row = g.start[lo] + first;
+  t.valid = last - first;
   t.n = (t.valid + kTokUnit - 1) / kTokUnit * kTokUnit;
   return t;
 }
