@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
   // saves the registers of the other kernel's flags)
   const bool has_y = ALL || p.y, post = ALL || p.w_post, next = ALL || p.dh,
              has_dout = ALL || p.dout;
-  const bool gate_all = p.gate && p.gate_tokens == 0, gate_each = p.gate && p.gate_tokens == 1;
+  const bool gate_all = p.gate && p.gate_tokens == 0, gate_each = p.gate && p.gate_tokens == 1,
+             gate_rows = p.gate && p.gate_tokens > 0;
   // (addresses are made from the parameters and one offset: registers are short)
   auto in = [](const void* q, size_t at) { return static_cast<const T*>(q) + at; };
   auto to = [](void* q, size_t at) { return static_cast<T*>(q) + at; };
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
   const uint32_t fpitch = (uint32_t)blockDim.x * EPT;
   unsigned char* mine = nsm + (size_t)group * p.ring_bytes;
   Ring ring(mine, p.slots * pitch, p.stages);
-  const bool running = post && p.gate && p.gate_tokens;
+  const bool running = post && gate_rows;
   // (addresses of what is used seldom are made where it is)
   auto ring_end = [&](int which) {
     return reinterpret_cast<float*>(nsm + (size_t)group * p.ring_bytes) + which * fpitch;
@@ -686,40 +687,30 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
         u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(v[e], both(-k2)));
       }
       cols.store(to(p.dy, at), u);
-      if (left == 0 || r + 1 == r1) {
+      if (gate_rows && (left == 0 || r + 1 == r1)) {
         // the gate row, or the worker's range, ends
         float2 g[P], wp[P];
+        gate_row(g, r);
+        post_weights(wp);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
           A[e] = mul2(A[e], both(p.b));
-          g[e] = both(1.0f);
+          wp[e] = mul2(wp[e], A[e]);
         }
-        if (p.gate) {
-          gate_row(g, r);
-          post_weights(wp);
-#pragma unroll
-          for (int e = 0; e < P; ++e) wp[e] = mul2(wp[e], A[e]);
-          const int gi = p.gate_tokens ? r / p.gate_tokens : 0;
-          const long long first = (long long)gi * p.gate_tokens;
-          const long long last = p.gate_tokens ? min(first + p.gate_tokens, (long long)p.n) : p.n;
-          if (gate_all)
-            cols.store_f32(ring_end(at_gate), wp);
-          else if (first < r0)
-            cols.store_f32(p.part_head + (size_t)w * p.pitch, wp);
-          else if (last > r1)
-            cols.store_f32(p.part_tail + (size_t)w * p.pitch, wp);
-          else
-            cols.store(static_cast<T*>(p.dgate) + (long long)gi * p.gate_stride, wp);
-        }
+        const int gi = r / p.gate_tokens;
+        const long long first = (long long)gi * p.gate_tokens;
+        const long long last = min(first + p.gate_tokens, (long long)p.n);
+        if (first < r0)
+          cols.store_f32(p.part_head + (size_t)w * p.pitch, wp);
+        else if (last > r1)
+          cols.store_f32(p.part_tail + (size_t)w * p.pitch, wp);
+        else
+          cols.store(static_cast<T*>(p.dgate) + (long long)gi * p.gate_stride, wp);
         if (running) {
           cols.load_f32(wp, extra(0));
 #pragma unroll
           for (int e = 0; e < P; ++e) wp[e] = fma2(g[e], A[e], wp[e]);
           cols.store_f32(extra(0), wp);
-        } else if (post) {  // (the range's end: the ring is done with)
-#pragma unroll
-          for (int e = 0; e < P; ++e) wp[e] = mul2(g[e], A[e]);
-          cols.store_f32(ring_end(at_post), wp);
         }
 #pragma unroll
         for (int e = 0; e < P; ++e) A[e] = both(0.0f);
@@ -727,10 +718,24 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
     }
     ring.done();
   }
+  // The ring takes the sums only when no thread reads rows from it any more: a
+  // thread's columns of fp32 lie where other threads' chunks did.
+  __syncthreads();
   if (next) cols.store_f32(ring_end(0), acc_n);
-  if (r0 == r1) {  // no rows: A is zeros
-    if (gate_all) cols.store_f32(ring_end(at_gate), A);
-    if (post && !running) cols.store_f32(ring_end(at_post), A);
+  if (has_y && !gate_rows) {
+    float2 v[P];
+#pragma unroll
+    for (int e = 0; e < P; ++e) A[e] = mul2(A[e], both(p.b));
+    if (gate_all) {
+      post_weights(v);
+#pragma unroll
+      for (int e = 0; e < P; ++e) v[e] = mul2(v[e], A[e]);
+      cols.store_f32(ring_end(at_gate), v);
+      cols.load(v, in(p.gate, 0));
+#pragma unroll
+      for (int e = 0; e < P; ++e) A[e] = mul2(v[e], A[e]);
+    }
+    if (post) cols.store_f32(ring_end(at_post), A);
   }
   __syncthreads();
   // the workers' sums, in their order

@@ -82,8 +82,9 @@ MOE_API moe_status moe_norm_backward(const moe_norm_config* cfg, const void* dre
  *   h[t]   = out[t] rstd_next[t] (w_next + weight_offset)  (w_next and h NULL: none)
  * with rstd the (mean square + eps)^-1/2 of y and of out. x, y, out, h [n,d];
  * gate [rows, d] with gate_stride; w_post, w_next [d] fp32; rstd_post,
- * rstd_next [n] fp32 (NULL: not stored). h is taken from out before out is
- * rounded. out may be x or y, h may be y or x (not both the same). */
+ * rstd_next [n] fp32 (NULL: not stored; stored with w_post / w_next only). h is
+ * taken from out before out is rounded. out may be x or y, h may be y or x (not
+ * both the same); no other overlap. */
 MOE_API moe_status moe_residual_norm_forward(const moe_norm_config* cfg, const void* x,
                                              const void* y, const float* w_post,
                                              const void* gate, const float* w_next, void* out,
@@ -122,14 +123,16 @@ MOE_API moe_status moe_grad_workspace_size(int count, size_t* bytes);
  * HOST array, read during the call; `out` members are ignored. Elements are
  * squared and summed so that values of any magnitude count (no overflow or
  * underflow before the root); partial sums are fp64 and joined in a fixed
- * order. An infinite element gives +inf, a NaN gives NaN. norm: device, fp32. */
+ * order. An infinite element gives +inf, a NaN gives NaN. A tensor listed twice
+ * counts twice. norm: device, fp32. */
 MOE_API moe_status moe_grad_norm(const moe_grad_tensor* tensors, int count, float* norm, void* ws,
                                  size_t ws_bytes, moe_stream_t stream);
 
 /* The norm, and the tensors scaled so that it is at most max_norm:
  * norm[0] as above, norm[1] = min(1, max_norm / (norm[0] + 1e-6)) (NaN if the
- * norm is), out = grad * norm[1], rounded once. max_norm >= 0. In place
- * (out == grad) and with norm[1] == 1 nothing is rewritten. */
+ * norm is), out = grad * norm[1], rounded once. max_norm >= 0. An out is its
+ * own grad (in place; with norm[1] == 1 nothing is rewritten) or memory that no
+ * other listed tensor touches. */
 MOE_API moe_status moe_grad_clip(const moe_grad_tensor* tensors, int count, float max_norm,
                                  float* norm, void* ws, size_t ws_bytes, moe_stream_t stream);
 

@@ -78,7 +78,7 @@ class Case:
             near(self.h, h, step * h.abs() + R.ROW * terms * r2[:, None] * w +
                  rel[:, None] * h.abs(), "h")
 
-    def backward(self, dx=None, dy=None, dout=True):
+    def backward(self, dx=None, dy=None, dout=True, poison=False):
         """gradients from the stored forward results"""
         f = dict(dtype=torch.float32, device=DEV)
         self.dx = self.empty() if dx is None else dx
@@ -90,6 +90,8 @@ class Case:
             self.dgate = torch.full((max(self.rows, 1), int(self.cfg.gate_stride)), 7.0,
                                     dtype=self.dt, device=DEV)[:self.rows, :self.d]
         self.ws = block.norm_workspace(self.cfg, DEV)
+        if poison:
+            self.ws.fill_(0xff)  # NaNs
         block.moe_residual_norm_backward(
             self.cfg, self.dout if dout else None, self.dh,
             self.out if self.w_next is not None else None, self.y, self.w_post, self.gate,
@@ -285,6 +287,26 @@ def test_same_sums_every_time_and_on_other_streams():
     s.synchronize()
     for a, b in zip(first, (c.dx, c.dy, c.dw_post, c.dgate, c.dw_next)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("tokens", [0, 1, 7])
+@pytest.mark.parametrize("n,d,dtype", [(3000, 7168, "bf16"), (4000, 4096, "bf16"),
+                                       (1500, 8192, "f32"), (6000, 1000, "bf16"),
+                                       (5000, 130, "f32"), (700, 16384, "bf16")])
+def test_every_worker_ends_well(n, d, dtype, tokens):
+    """Many rows a worker, so that its warps reach the end of their range apart,
+    several times over a poisoned workspace: the sums that are joined there are
+    those of the reference, and the same each time."""
+    c = Case(n, d, dtype, tokens, seed=n)
+    c.forward()
+    ref, mag = c.reference(), c.reference(magnitudes=True)
+    first = None
+    for _ in range(4):
+        c.backward(poison=True)
+        c.check_backward(ref, mag)
+        got = [t.clone() for t in (c.dx, c.dy, c.dw_post, c.dgate, c.dw_next)]
+        assert first is None or all(torch.equal(a, b) for a, b in zip(first, got))
+        first = got
 
 
 def test_captured_and_replayed():
