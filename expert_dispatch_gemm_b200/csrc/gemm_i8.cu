@@ -218,11 +218,13 @@ __device__ __forceinline__ float activate(float v) {
   if (ACT == A_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
   return v;
 }
-// (bf16 outputs take the fast exponential: its error is far below their step)
+// (bf16 outputs take the fast exponential and division: their errors, a few fp32
+// steps, are far below the output's; the exact division alone took as long as
+// the rest of the epilogue)
 template <typename OUT>
 __device__ __forceinline__ float silu_times(float u, float v) {
-  const float e = sizeof(OUT) == 2 ? __expf(-u) : expf(-u);
-  return u * __frcp_rn(1.0f + e) * v;
+  if (sizeof(OUT) == 2) return __fdividef(u, 1.0f + __expf(-u)) * v;
+  return u * __frcp_rn(1.0f + expf(-u)) * v;
 }
 
 // Epilogue of bf16 outputs. A lane of the accumulator is a channel, a row of
