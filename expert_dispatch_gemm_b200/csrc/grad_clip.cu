@@ -3,15 +3,15 @@
 //   norm = (sum_i sum_j g_ij^2)^1/2      c = min(1, max_norm / (norm + 1e-6))
 //   out_i = c g_i
 //
-// Two passes over the data, since c needs every element: the floor is one
-// read and one write, and the second read on top of it is kept small by the
-// order. Each tensor is cut into equal tiles of up to 8,192 elements; the norm
-// pass deals them out to its blocks in turn, and the scaling pass takes them
-// from the last one backwards, so it begins with what the norm pass read last,
-// which the 126 MB L2 still holds. Both passes are bound by HBM. On a B200, 806 MB
-// of bf16 gradients: 118 us for the norm (the copy rate), 360 us with the clip, where
-// two reads and a write take 369 us at the copy rate; a scaling pass of resident
-// blocks that walk many tiles took 40 us more (its accesses lie further apart).
+// Two passes over the data, since c needs every element: two reads and a write,
+// where the floor is one of each. Each tensor is cut into equal tiles of up to
+// 8,192 elements; the norm pass deals them out to its blocks in turn, and the
+// scaling pass takes them from the last one backwards, beginning with what the
+// norm pass read last (small lists still lie in L2 whole). Both passes are bound
+// by HBM. On a B200, 806 MB of bf16 gradients: 118 us for the norm (the copy
+// rate), 361 us with the clip, where two reads and a write take 369 us at the copy
+// rate; a scaling pass of resident blocks that walk many tiles took 40 us more
+// (its accesses lie further apart).
 //
 // Squares: eight neighbours are summed in fp32 when the largest of them lies
 // in [2^-50, 2^50] (or all are 0), where neither the squares nor their sum
