@@ -27,10 +27,11 @@
 // - the next rows' chunks come into shared memory by cp.async while a row is
 //   computed; each thread reads back only what it copied itself, so no barrier
 //   guards the ring, and the only barriers are those of the row sums.
-// On a B200: forward, n 8192, d 7168 bf16, 80.6 us (5.8 TB/s, 89% of a copy's
-// rate; the first version, a block a row with plain loads, took 132); backward, n
-// 16384, d 2048 bf16, 70 us (5.7 TB/s, 88%; 138), n 8192, d 7168 151 us (71%: one
-// worker an SM, whose warps wait for each other at every row).
+// On a B200, replayed from a graph: forward, n 8192, d 7168 bf16, 81 to 83 us
+// (5.7 TB/s, 87 to 89% of a copy's rate; without the ring and the packed pairs
+// 112); backward, n 16384, d 2048 bf16, one gate row, 70 to 72 us (5.6 TB/s, 86 to
+// 88%), n 8192, d 7168 151 us (71%: one worker an SM, whose warps wait for each
+// other at every row).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -769,8 +770,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
 // partial rows, then the slices. blockIdx.y: dw_post, dw_next, then the gate: its
 // one row, or the rows that more than one worker holds, found by row (fewer
 // rows than workers) or by the worker that they begin in. Rows that span a few
-// workers only are a slice's work each, 32 to a block (at n 16384, d 2048, 3 tokens
-// a gate row, a block each took 95 us).
+// workers only are a slice's work each, 32 to a block (n 16384, d 2048, 3 tokens
+// a gate row: the whole backward 106 us, with a block for each 200).
 struct NormReduce {
   NormBwd b;
   int by_group;

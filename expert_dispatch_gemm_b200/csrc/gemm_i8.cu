@@ -32,8 +32,8 @@
 // bytes): k 14336, 1,280 rows a group 3.0 POP/s (91%); SwiGLU, k 4096, 802 us for
 // 10,240 rows and 14,336 units (90%; its epilogue is not overlapped, 70 us of it);
 // k 1024, 2,048 rows a group, 262 us for 131,072 rows and 2,048 channels (64%: the
-// SMs' path to L2, see the epilogue); 16 rows a group of 32, k 7168, SwiGLU 2048, 154
-// us (94% of the HBM rate).
+// SMs' path to L2, see the epilogue); 16 rows a group of 32, k 7168, SwiGLU 2048,
+// 148 to 154 us (94 to 97% of the HBM rate).
 // Every mbarrier wait is bounded; on a timeout a role records the error, its
 // copies and MMAs in flight are waited for (bounded), TMEM is freed and the
 // kernel returns.
@@ -753,8 +753,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // same result: the tile's 32-row chunks are dealt out to the pairs, each CTA
 // sends its sums of the others' chunks into their rings (free by then) through
 // distributed shared memory, adds what it received to its own, and writes. One
-// row, weights from HBM: k 2048, 7,168 channels 9.2 us (unsplit 13), k 7168, 2,048
-// channels 11.7 us (34), where the smallest product of all takes 5.6.
+// row, weights from HBM: k 2048, 7,168 channels (28 tiles, 2 parts) 9.3 us, unsplit
+// 10.7; k 7168, 2,048 channels (8 tiles, 4 parts) 11.7 us, unsplit 25.3. The
+// smallest product of all takes 5.6.
 // ---------------------------------------------------------------------------
 constexpr int kSplitRing = 192 * 1024;
 constexpr int kSplitStages = 6;  // of 32 KB; SwiGLU 4 of 48 KB
