@@ -574,7 +574,9 @@ class Block:
             p, g = self.p, {"dx": torch.empty_like(self.out), "dy": torch.empty_like(self.out),
                             "dw_pre": torch.empty_like(self.p["w_pre"])}
             for k in ("w_post", "gate", "w_next"):
-                g["d" + k] = None if p.get(k) is None else torch.empty_like(p[k])
+                t = p.get(k)  # (a gate's gradient has the gate's stride between rows)
+                g["d" + k] = None if t is None else torch.empty_strided(
+                    t.shape, t.stride(), dtype=t.dtype, device=t.device)
             self._nws = norm_workspace(self.cfg, self.out.device)
             g["layer"] = self.layer.grads()
             self._g = g
@@ -603,7 +605,9 @@ class Block:
             g = self.grads()
             own = [g[k] for k in ("dw_pre", "dw_post", "dgate", "dw_next")]
             own += [t for k, t in g["layer"].items() if k not in ("dX", "dL")]
-            glist = grad_list([t for t in own if t is not None])
+            own = [t for t in own if t is not None]
+            # what lies between the rows of a strided gate's gradient is no gradient
+            glist = grad_list([r for t in own for r in ([t] if t.is_contiguous() else t.unbind())])
             self._clip = (glist, torch.empty(2, dtype=torch.float32, device=self.out.device),
                           grad_workspace(glist, self.out.device))
         glist, norm, ws = self._clip

@@ -120,6 +120,36 @@ def test_block_without_optional_parts():
     assert b.clip_grads(1.0)[1].item() < 1.0
 
 
+@pytest.mark.parametrize("tokens", [1, 100])
+def test_gate_that_is_a_slice_of_wider_rows(tokens):
+    """A gate with a stride (one of several parts of a modulation's rows): the
+    same bits as its dense copy gives, backward and clip included."""
+    w = wl.SMALL[3]
+    res = []
+    for wide in (False, True):
+        b, p, x, dout, dh = make(w, tokens=tokens)
+        rows = p["gate"].shape[0]
+        if wide:
+            parts = torch.full((rows, 3 * w.d), float("nan"), dtype=w.torch_dtype, device=DEV)
+            parts[:, w.d:2 * w.d] = p["gate"]
+            p["gate"] = parts[:, w.d:2 * w.d]
+            b = block.Block(moe.Layer(w, b.layer.inp, DEV), p, eps=1e-5, gate_tokens=tokens,
+                            block_scale=0.5, gate_stride=3 * w.d)
+        out, h_next = b.forward_train(x)
+        g = b.backward_train(dout, dh)
+        own = [g[k] for k in ("dx", "dy", "dw_pre", "dw_post", "dgate", "dw_next")]
+        res.append([out.clone(), h_next.clone()] + [t.clone() for t in own])
+        total = math.sqrt(sum(float((t.double() ** 2).sum()) for t in own[2:] + [
+            t for k, t in g["layer"].items() if t is not None and k not in ("dX", "dL")]))
+        norm, factor = b.clip_grads(0.25 * total).tolist()
+        # (the list's squares are added in fp64; 10 roundings as in test_train_step)
+        assert abs(norm - total) <= 10 * R.U * total
+        near(g["dgate"], res[-1][6].double() * (0.25 * total / (total + 1e-6)),
+             14 * R.U * res[-1][6].double().abs(), R.half_step(w.torch_dtype), "clipped gate")
+    for i, (s, t) in enumerate(zip(*res)):
+        assert torch.equal(s, t), i
+
+
 def test_serving_with_8_bit_experts():
     w = wl.SMALL[4]
     inp = wl.make_inputs(w, DEV)
