@@ -1211,13 +1211,21 @@ moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq, const fl
   p.mt_tiles = (cfg->n_out + 255) / 256;
   p.out = out;
   p.err = static_cast<int*>(ws);
-  // A bound on the tiles. Few of them leave most SMs idle: K is then split, over
-  // as many pairs as the machine has for each (clusters of 8 and of 4 CTAs do
-  // not fill every GPC, so not quite up to 74 pairs), two K blocks each at least.
+  // A bound on the tiles. Few of them leave most SMs idle: a long K is then split
+  // over the pairs of a cluster, as far as all clusters are resident at once:
+  // they do not fill every GPC, and a second round costs more than the split
+  // saves. Measured, one row, weights from HBM, us in 1 / 2 / 4 parts:
+  //   k 7168, 15 tiles 25.5 / 16.2 / 12.8, 16 tiles 25.7 / 16.2 / 23.1;
+  //   k 4096, 33 tiles 17.0 / 13.4 / 27.6, 34 tiles 17.1 / 23.3 / 27.7
+  // (the limits keep one or so in hand). A short K loses to the two barriers of the
+  // cluster and the exchange: 8 tiles, k 1024 6.8 / 7.7 / 7.6, k 2048 9.4 / 8.7 / 8.1;
+  // SwiGLU exchanges twice the sums: 32 tiles, k 2048 11.8 / 12.6, k 4096 18.7 / 18.6.
   const long long tiles =
       ((long long)cfg->rows + (kMaxTok - 1LL) * cfg->groups) / kMaxTok * p.mt_tiles;
   const int kblocks = (cfg->k + kBK - 1) / kBK;
-  p.parts = tiles <= 16 && kblocks >= 8 ? 4 : tiles <= 32 && kblocks >= 4 ? 2 : 1;
+  p.parts = tiles <= 14 && kblocks >= 16                  ? 4
+            : tiles <= 32 && kblocks >= (swiglu ? 32 : 16) ? 2
+                                                           : 1;
   cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = cfg->dtype == MOE_BF16
                             ? run_gemm<__nv_bfloat16>(x, mw, mw3, mo, cfg->act, p, (int)tiles, s)

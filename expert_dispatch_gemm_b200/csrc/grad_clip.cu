@@ -45,7 +45,8 @@ __host__ __device__ inline int tile_count(long long n) { return (int)((n + kTile
 
 // The tensors of one launch travel in its parameters: 4 KB of them hold what
 // one layer has, the largest parameter block (32,764 bytes) what an unstacked
-// expert list has.
+// expert list has (5 tensors in it: 14.3 us a clip, one after another, against
+// 11.4; a long list in blocks of 120 would be two launches for each).
 template <int CAP>
 struct GradBatch {
   GradTensor t[CAP];

@@ -19,8 +19,8 @@
 //   exact where s is), and no element needs a check.
 // Bound by HBM: it reads each element once and writes one byte for it. On a B200,
 // bf16, buffers in turn so that none is in L2: 10240 x 4096 in 23.6 us (5.3 TB/s,
-// 81% of a copy's rate), 131072 x 1024 in 80 us (5.0 TB/s, 77%); with fp32's
-// remainder check for bf16 too 31.9 and 91 us.
+// 81% of a copy's rate; with fp32's remainder check for bf16 too 31.9), 131072 x
+// 1024 in 72 us (5.6 TB/s, 85%).
 //
 // "Expert choice routing" (aicassindra.com), "The math": X_in[e] = P[e] X. A
 // permutation of rows commutes with a scale per row, so the dispatch gathers
@@ -352,13 +352,16 @@ cudaError_t run_quant(const QuantArgs& a, int threads, cudaStream_t s) {
                     s, a);
 }
 
-// A warp a row while a lane holds at most 4 vectors, then a block a row with
-// up to 4 vectors a thread.
+// A warp a row while a lane holds up to 2 vectors (4 of fp32), then a block a row
+// with up to 4 vectors a thread. 131072 rows, us, warp against block: bf16 512
+// columns 37.9 / 50.8 (with room for 4 vectors a lane 54.0), 1024 columns, 4 vectors,
+// 78.7 / 71.8; fp32 256 columns 32.9 / 48.5, 512 columns, 4 vectors, 58.4 / 64.1.
 template <typename T, int VEC>
 cudaError_t launch_quant(const QuantArgs& a, cudaStream_t s) {
   const int chunks = a.cols / VEC;
   if (chunks <= 32) return run_quant<T, VEC, 1, false>(a, 32 * kQWarps, s);
-  if (chunks <= 32 * 4) return run_quant<T, VEC, 4, false>(a, 32 * kQWarps, s);
+  if (chunks <= 32 * 2) return run_quant<T, VEC, 2, false>(a, 32 * kQWarps, s);
+  if (VEC < 8 && chunks <= 32 * 4) return run_quant<T, VEC, 4, false>(a, 32 * kQWarps, s);
   if (chunks <= 1024 * 4)
     return run_quant<T, VEC, 4, true>(a, ((chunks + 3) / 4 + 31) / 32 * 32, s);
   return run_quant<T, VEC, 0, true>(a, 1024, s);

@@ -215,6 +215,33 @@ def test_split_reduction(k, o, starts, counts, rows, dtype, act):
     c.check()
 
 
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "swiglu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("k,o,starts,counts,rows", [
+    (2048, 256, [0], [256], 256),                   # the longest tile, K in four
+    (2064, 272, [0], [193], 193),                   # a K block that ends early
+    (2064, 3584, [3], [1], 4),                      # as many tiles as are split in four
+    (2064, 3600, [0], [70], 128),                   # one more, K in two (SwiGLU: whole)
+    (4112, 1936, [0, 100, 250], [100, 150, 33], 283),
+    (4096, 8192, [2], [5], 9),                      # as many as are split in two
+    (4096, 8208, [2], [5], 9),                      # one more
+    (4096, 64, [5], [0], 128),                      # no rows at all
+    (16384, 256, [0, 7], [7, 1], 8),
+])
+def test_split_of_a_long_reduction(k, o, starts, counts, rows, dtype, act):
+    """Both sides of each limit within which K is split."""
+    c = Gemm(rows, k, o, act, dtype, starts, counts, len(starts), seed=rows + k + o)
+    c.run()
+    c.check()
+
+
+@pytest.mark.parametrize("dtype,cols", [("bf16", c) for c in (256, 264, 496, 504, 512, 1024)] +
+                         [("f32", c) for c in (128, 132, 508, 512, 516)])
+@pytest.mark.parametrize("rows", [1, 37, 5000])
+def test_quantize_rows_about_a_warps_share(rows, cols, dtype):
+    test_quantize_rows(rows, cols, dtype)
+
+
 def test_many_groups():
     counts = [(7 * g) % 41 for g in range(260)]
     starts, at = [], 0
