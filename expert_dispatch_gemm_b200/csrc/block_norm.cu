@@ -16,7 +16,10 @@
 // m needs D, which needs mean(q u); expanding D gives m from sums that one
 // pass over the row collects together,
 //   m = (sum (dout + r2 q) c - r2 mean(q u) sum u c) / d,
-// so a row takes one block reduction (of three sums), not two in sequence.
+// so a row takes one block reduction (of three sums), not two in sequence. All of
+// it is computed from u and yr, never from y with powers of r1: yr is about 1
+// whatever y and eps are, where r1^3 leaves fp32's range for |y| above 4e12, and
+// for rows of zeros with eps below 2e-26.
 //
 // The forward moves 4 n d elements (x, y, out, h), the backward 6 n d: both are
 // to be bound by HBM, which leaves about 20 instructions an element. So
@@ -661,7 +664,13 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
       if (STAGED) cols.load_smem(v, ring.read + s_y);
       else cols.load(v, in(p.y, at));
     };
-    if (has_y) load_y();
+    if (has_y) {
+      load_y();
+      if (post) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] = mul2(v[e], both(rp));  // yr
+      }
+    }
     if (next || post) {
       float2 s2 = both(0.0f), s3 = both(0.0f);
       if (post) {
@@ -675,8 +684,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
       float a2 = s2.x + s2.y, a3 = s3.x + s3.y;
       // two buffers: a warp may still read row r's while row r + 1 is written
       worker_sum3(k1, a2, a3, red[r & 1] + group * warps, warps);
-      k1 *= rn * inv_d;                            // r2 mean(q u)
-      k2 = rp * rp * rp * (a2 - k1 * a3) * inv_d;  // r1^2 mean(D c); 0 without the norm
+      k1 *= rn * inv_d;                  // r2 mean(q u)
+      k2 = (a2 - k1 * a3) * inv_d * rp;  // r1 mean(D c)
       if (has_y && !KEEP) load_y();
     }
 #pragma unroll
@@ -688,8 +697,9 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
     if (has_y) {
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        A[e] = fma2(t[e], mul2(v[e], both(rp)), A[e]);
-        u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(v[e], both(-k2)));
+        const float2 yr = KEEP || !post ? v[e] : mul2(v[e], both(rp));
+        A[e] = fma2(t[e], yr, A[e]);
+        u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(yr, both(-k2)));
       }
       cols.store(to(p.dy, at), u);
       if (gate_rows && (left == 0 || r + 1 == r1)) {

@@ -33,7 +33,11 @@
 extern "C" {
 #endif
 
-/* ---- residual norms ---------------------------------------------------- */
+/* ---- residual norms ----------------------------------------------------
+ * A row's sum of squares is fp32: it has to fit (a root mean square below
+ * 1.8e19 / d^1/2); squares below 2^-126 count in steps of 2^-149, beside eps.
+ * Rows of any size in between, zeros among them, and any eps give the gradients
+ * of their formulas, as far as those fit the outputs' type. */
 
 #define MOE_NORM_MAX_D 16384
 
