@@ -699,7 +699,8 @@ __global__ void __launch_bounds__(MAXT) norm_bwd_kernel(const NormBwd p) {
       for (int e = 0; e < P; ++e) {
         const float2 yr = KEEP || !post ? v[e] : mul2(v[e], both(rp));
         A[e] = fma2(t[e], yr, A[e]);
-        u[e] = fma2(mul2(t[e], cw[e]), both(rp), mul2(yr, both(-k2)));
+        u[e] = mul2(t[e], cw[e]);
+        if (post) u[e] = fma2(u[e], both(rp), mul2(yr, both(-k2)));
       }
       cols.store(to(p.dy, at), u);
       if (gate_rows && (left == 0 || r + 1 == r1)) {

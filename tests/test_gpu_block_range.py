@@ -3,6 +3,7 @@ the way to a result that does not."""
 import pytest
 import torch
 
+import block_ref as R
 from test_gpu_block_norm import Case
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +43,14 @@ def test_norm_backward_of_zero_rows_under_a_small_eps(d, dtype, eps):
     for t in (c.dx, c.dy, c.dgate, c.dw_post, c.dw_next):
         assert torch.isfinite(t).all()
     c.check_backward(c.reference(), c.reference(magnitudes=True))
+
+
+def test_a_block_output_that_is_not_finite_does_not_reach_dy_without_its_norm():
+    """Without w_post dy = b g D: y is no part of it."""
+    c = Case(6, 96, "f32", 2, post=False, nxt=False, b=0.5, seed=3)
+    c.y[2, 5] = float("inf")
+    c.y[3, 7] = float("nan")
+    c.forward()
+    c.backward()
+    ref = 0.5 * c.dout.double() * R.gate_of(c.gate, 6, 2)
+    assert bool(((c.dy.double() - ref).abs() <= 3 * R.U * ref.abs()).all())
