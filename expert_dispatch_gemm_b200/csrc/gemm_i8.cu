@@ -254,11 +254,14 @@ __device__ __forceinline__ uint32_t swizzled(int row, int piece) {
   return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4);
 }
 
-__device__ __forceinline__ float2 scaled(uint32_t a, uint32_t b, float2 s) {
-  return __fmul2_rn(make_float2((float)(int)a, (float)(int)b), s);
+// Sums times the channel's scale, then the rows': the scales' own product may
+// leave fp32's range where the result does not.
+__device__ __forceinline__ float2 scaled(uint32_t a, uint32_t b, float2 xs, float ws) {
+  return __fmul2_rn(
+      __fmul2_rn(make_float2((float)(int)a, (float)(int)b), make_float2(ws, ws)), xs);
 }
-__device__ __forceinline__ float2 pair_scale(float2 xs, float ws) {
-  return __fmul2_rn(xs, make_float2(ws, ws));
+__device__ __forceinline__ float scaled(uint32_t a, float xs, float ws) {
+  return (float)(int)a * ws * xs;
 }
 
 // The 8 x 8 blocks r[j][k] (rows 8 j .., channels 8 k ..) of rows cc .. cc + 15 of
@@ -330,7 +333,7 @@ __device__ __forceinline__ void finish(uint32_t (&r)[2][4], const uint32_t (&lo)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t* v = (k < 2 ? lo : hi) + 4 * j + 2 * (k & 1);
-      const float2 u = scaled(v[0], v[1], pair_scale(x, ws[k]));
+      const float2 u = scaled(v[0], v[1], x, ws[k]);
       r[j][k] = pack_bf16x2(activate<ACT>(u.x), activate<ACT>(u.y));
     }
   }
@@ -347,8 +350,8 @@ __device__ __forceinline__ void finish_gated(uint32_t (&r)[2][4], const uint32_t
     for (int k = 0; k < 4; ++k) {
       const int at = 4 * j + 2 * (k & 1);
       const uint32_t *uu = (k < 2 ? ulo : uhi) + at, *vv = (k < 2 ? vlo : vhi) + at;
-      const float2 u = scaled(uu[0], uu[1], pair_scale(x, ws1[k]));
-      const float2 v = scaled(vv[0], vv[1], pair_scale(x, ws3[k]));
+      const float2 u = scaled(uu[0], uu[1], x, ws1[k]);
+      const float2 v = scaled(vv[0], vv[1], x, ws3[k]);
       r[j][k] = pack_bf16x2(silu_times<__nv_bfloat16>(u.x, v.x),
                             silu_times<__nv_bfloat16>(u.y, v.y));
     }
@@ -540,7 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sm100::tmem_ld_32x32b_x32(tbase + cc, v);
           sm100::tmem_ld_wait();
           emit_f32<32>(xsc, p, t, cc, col0, lane, [&](int i, float xs) {
-            return activate<ACT>((float)(int)v[i] * (xs * ws[0]));
+            return activate<ACT>(scaled(v[i], xs, ws[0]));
           });
         }
       }
@@ -726,8 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           sm100::tmem_ld_32x32b_x16(tbase + 256u + at, v);
           sm100::tmem_ld_wait();
           emit_f32<16>(xsc, p, t, at, col0, lane, [&](int i, float xs) {
-            return silu_times<OUT>((float)(int)u[i] * (xs * ws1[0]),
-                                   (float)(int)v[i] * (xs * ws3[0]));
+            return silu_times<OUT>(scaled(u[i], xs, ws1[0]), scaled(v[i], xs, ws3[0]));
           });
         }
       }
@@ -991,10 +993,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 2; ++e) {
               const int at = 4 * j + 2 * (k4 & 1) + e, i = 8 * j + 2 * (lane & 3) + e;
               const int c = col0 + (lane >> 2) + 8 * k4;
-              const float a = (float)(int)(k4 < 2 ? lo[0] : hi[0])[at] * (xs[i] * ws1[k4]);
+              const float a = scaled((k4 < 2 ? lo[0] : hi[0])[at], xs[i], ws1[k4]);
               float v;
               if constexpr (SIDES == 2)
-                v = silu_times<OUT>(a, (float)(int)(k4 < 2 ? lo[1] : hi[1])[at] * (xs[i] * ws3[k4]));
+                v = silu_times<OUT>(a, scaled((k4 < 2 ? lo[1] : hi[1])[at], xs[i], ws3[k4]));
               else
                 v = activate<ACT>(a);
               if (16 * u + i < t.valid && c < p.n_out)

@@ -187,12 +187,12 @@ MOE_API moe_status moe_gemm_i8_workspace_size(const moe_gemm_i8_config* cfg, siz
  *   out[r,o] = act(u[r,o]), or silu(u) v with v from w3 / w3_scale (SwiGLU)
  * x: xq [rows,k] int8, x_scale [rows] fp32; w, w3 [groups,n_out,k] int8,
  * w_scale, w3_scale [groups,n_out] fp32; out [rows,n_out]. The sum over j is
- * exact (int32); scales and activation are fp32, rounded once into out. Rows
- * outside every group are left as they were. starts and counts NULL: one
- * group (groups == 1) of all `rows` rows. Groups must lie in ascending order
- * inside [0, rows) and not overlap; a group that does not fit is cut to what
- * does. Rows start anywhere (no alignment). xq, w, w3 and out 16-byte
- * aligned. */
+ * exact (int32); scales (the sum times w_scale, then times x_scale) and
+ * activation are fp32, rounded once into out. Rows outside every group are left
+ * as they were. starts and counts NULL: one group (groups == 1) of all `rows`
+ * rows. Groups must lie in ascending order inside [0, rows) and not overlap; a
+ * group that does not fit is cut to what does. Rows start anywhere (no
+ * alignment). xq, w, w3 and out 16-byte aligned. */
 MOE_API moe_status moe_gemm_i8(const moe_gemm_i8_config* cfg, const int8_t* xq,
                                const float* x_scale, const int32_t* starts,
                                const int32_t* counts, const int8_t* w, const float* w_scale,
