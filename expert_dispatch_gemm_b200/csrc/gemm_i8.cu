@@ -224,13 +224,18 @@ __device__ __forceinline__ float activate(float v) {
   if (ACT == A_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
   return v;
 }
+// silu(u) v with e = exp(-|u|): u / (1 + e), times e where u < 0. exp(-u) would
+// pass fp32's range at u = -88.7, where the value is 1e-37 v, and from -87.3 on the
+// fast division by it gives zero. (131,072 rows, k 1024, 1,024 units: 270 us, with
+// exp(-u) 266.)
 // (bf16 outputs take the fast exponential and division: their errors, a few fp32
 // steps, are far below the output's; the exact division alone took as long as
 // the rest of the epilogue)
 template <typename OUT>
 __device__ __forceinline__ float silu_times(float u, float v) {
-  if (sizeof(OUT) == 2) return __fdividef(u, 1.0f + __expf(-u)) * v;
-  return u * __frcp_rn(1.0f + expf(-u)) * v;
+  const float e = sizeof(OUT) == 2 ? __expf(-fabsf(u)) : expf(-fabsf(u));
+  const float n = u < 0.0f ? u * e : u;
+  return (sizeof(OUT) == 2 ? __fdividef(n, 1.0f + e) : n * __frcp_rn(1.0f + e)) * v;
 }
 
 // Epilogue of bf16 outputs. A lane of the accumulator is a channel, a row of

@@ -59,3 +59,28 @@ def test_scales_whose_product_overflows(rows, k, o, dtype):
     c.x.zero_()
     c.run()
     assert not c.out.any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,k,o", SHAPES)
+def test_silu_of_large_negative_sums(rows, k, o, dtype):
+    """silu(u) = u e^u / (1 + e^u) from u = -80 down to -100 is 1e-33 to 1e-42,
+    and counts where v is large."""
+    c = wide(rows, k, o, "swiglu", dtype, 1.0, 1.0, 1.0, rows + k)
+    c.w.neg_()
+    c.xs.fill_(1.0)
+    total = (c.x.double() @ c.w[0].double().T)[0]  # row 0's sums set the channels' scales
+    c.x.copy_(c.x[:1].expand_as(c.x))
+    c.ws.copy_((torch.linspace(-80, -100, o, device="cuda", dtype=torch.float64) / total)[None])
+    c.s3.fill_(1e25)
+    c.run()
+    u, v = products(c)
+    # e^u with u rounded three times and e^x's own error relative to |u| (see
+    # Gemm.check); below 2^-126 a value keeps steps of 2^-149, some of them
+    # (e^u, u e^u) before v multiplies them
+    want = R.act("swiglu", u, v)
+    tol = R.half_step(c.dt) * want.abs() + (20 + 5 * u.abs()) * R.U * want.abs() + \
+        (u.abs() + 2) * 2.0 ** -149 * v.abs()
+    off = (c.out.double() - want).abs() - tol
+    assert bool((off <= 0).all()), (off.max().item(), want.abs().max().item())
+    assert bool((c.out[:, u[0] > -87] != 0).all())
