@@ -247,11 +247,12 @@ __global__ void __launch_bounds__(kClipThreads, 6)
                       float max_norm, float* norm, int write_norm) {
   __shared__ double red[kClipThreads / 32];
   pdl_wait();
-  const double r = total_norm(partial, count, red);
-  const double k = (double)max_norm / (r + 1e-6);
-  const float c = isnan(r) ? (float)r : (float)(k < 1.0 ? k : 1.0);
+  // the factor is of the norm as it is returned, +inf above the largest fp32
+  const float r = (float)total_norm(partial, count, red);
+  const double k = (double)max_norm / ((double)r + 1e-6);
+  const float c = isnan(r) ? r : (float)(k < 1.0 ? k : 1.0);  // (no limit: 1, of inf too)
   if (write_norm && blockIdx.x == 0 && threadIdx.x == 0) {
-    norm[0] = (float)r;
+    norm[0] = r;
     norm[1] = c;
   }
   for (int tile = b.tiles - 1 - (int)blockIdx.x; tile >= 0; tile -= gridDim.x) {

@@ -127,16 +127,17 @@ MOE_API moe_status moe_grad_workspace_size(int count, size_t* bytes);
  * HOST array, read during the call; `out` members are ignored. Elements are
  * squared and summed so that values of any magnitude count (no overflow or
  * underflow before the root); partial sums are fp64 and joined in a fixed
- * order. An infinite element gives +inf, a NaN gives NaN. A tensor listed twice
- * counts twice. norm: device, fp32. */
+ * order. An infinite element, or a norm above the largest fp32, gives +inf, a
+ * NaN gives NaN. A tensor listed twice counts twice. norm: device, fp32. */
 MOE_API moe_status moe_grad_norm(const moe_grad_tensor* tensors, int count, float* norm, void* ws,
                                  size_t ws_bytes, moe_stream_t stream);
 
 /* The norm, and the tensors scaled so that it is at most max_norm:
  * norm[0] as above, norm[1] = min(1, max_norm / (norm[0] + 1e-6)) (NaN if the
- * norm is), out = grad * norm[1], rounded once. max_norm >= 0. An out is its
- * own grad (in place; with norm[1] == 1 nothing is rewritten) or memory that no
- * other listed tensor touches. */
+ * norm is), out = grad * norm[1], rounded once. max_norm >= 0; +inf is no limit,
+ * norm[1] is 1 then unless the norm is NaN. An out is its own grad (in place;
+ * with norm[1] == 1 nothing is rewritten) or memory that no other listed tensor
+ * touches. */
 MOE_API moe_status moe_grad_clip(const moe_grad_tensor* tensors, int count, float max_norm,
                                  float* norm, void* ws, size_t ws_bytes, moe_stream_t stream);
 
