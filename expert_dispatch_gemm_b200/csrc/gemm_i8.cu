@@ -1074,19 +1074,6 @@ constexpr size_t smem_bytes(int ring) {
   return (size_t)ring + kEpiWarps * (sizeof(Staging) + sizeof(Scales)) + sizeof(State) + 1024;
 }
 
-// Raises the kernel's shared-memory limit, once on each device.
-template <class K>
-cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 template <auto kern, class... Args>
 cudaError_t launch_i8(int pairs, size_t bytes, cudaStream_t s, const Args&... args) {
   static std::atomic<uint64_t> done{0};
