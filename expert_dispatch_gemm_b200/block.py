@@ -493,6 +493,10 @@ class QuantizedLayer:
             _check(gemm_i8_validate(c), "moe_gemm_i8_validate")
         self.Wg, self.logit_bias = inputs["Wg"], inputs.get("logit_bias")
         self.sel_bias = inputs.get("sel_bias")
+        dev = _device_of(self.Wg)  # (moe_route's binding checks none of its operands)
+        _ptr(self.Wg, "Wg", _F32, (cfg.d, cfg.E), dev)
+        _opt(self.logit_bias, "logit_bias", _F32, (cfg.E,), dev)
+        _opt(self.sel_bias, "sel_bias", _F32, (cfg.E,), dev)
         self.W1, self.s1 = quantize_weights(inputs["W1"], inputs.get("sW1"))
         self.W2, self.s2 = quantize_weights(inputs["W2"], inputs.get("sW2"))
         self.W3, self.s3 = (quantize_weights(inputs["W3"], inputs.get("sW3"))
@@ -511,6 +515,7 @@ class QuantizedLayer:
         self.out = torch.empty((w.n, w.d), dtype=dt, device=device)
 
     def forward(self, X, stream=None):
+        _ptr(X, "X", self.out.dtype, self.out.shape, _device_of(self.out))
         moe.moe_route(self.cfg, X, self.Wg, self.logit_bias, self.sel_bias, self.route, self.ws,
                       stream)
         moe_dispatch_i8(self.dispatch_cfg, X, self.route, self.Xq, self.xs, self.starts,
