@@ -13,6 +13,7 @@ gradients; ``QuantizedLayer`` serves a layer with 8-bit experts.
 from __future__ import annotations
 
 import bisect
+import contextlib
 import ctypes
 import os
 
@@ -161,14 +162,18 @@ def _ws(ws, dev):
     return _ptr(ws, "ws", torch.uint8, (ws.numel(),), dev)
 
 
+def _check_stream(stream, dev):
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is of {stream.device}, the tensors are on cuda:{dev}")
+
+
 def _call(what, dev, stream, *args):
     """The entry point on the tensors' device and stream; raises MoeError."""
     fn = (_FN or _functions())[what]
     if stream is None:
         raw = torch._C._cuda_getCurrentRawStream(dev)
     else:
-        if stream.device.index != dev:
-            raise ValueError(f"the stream is of {stream.device}, the tensors are on cuda:{dev}")
+        _check_stream(stream, dev)
         raw = stream.cuda_stream
     if dev == torch._C._cuda_getDevice():
         status = fn(*args, raw)
@@ -177,6 +182,19 @@ def _call(what, dev, stream, *args):
             status = fn(*args, raw)
     if status != MOE_OK:
         raise MoeError(status, what)
+
+
+_NOTHING = contextlib.nullcontext()
+
+
+def _on(dev, stream):
+    """The device and the stream of a sequence of calls, made current for it: the
+    layer's calls (moe.py) take the current device as theirs, and a buffer made on
+    the way belongs to the stream that it is used on."""
+    if stream is not None:
+        _check_stream(stream, dev)
+        return torch.cuda.stream(stream)
+    return _NOTHING if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _check(status: int, what: str):
@@ -502,7 +520,8 @@ class QuantizedLayer:
         self.W3, self.s3 = (quantize_weights(inputs["W3"], inputs.get("sW3"))
                             if w.act == "swiglu" else (None, None))
         self.route = RouteBuffers(cfg, device)
-        self.ws = moe.workspace(cfg, device, layer=False)
+        with _on(dev, None):
+            self.ws = moe.workspace(cfg, device, layer=False)
         f32, i32, i8 = torch.float32, torch.int32, torch.int8
         self.Xq = torch.empty((sz.rows, cfg.d), dtype=i8, device=device)
         self.xs = torch.empty(sz.rows, dtype=f32, device=device)
@@ -515,18 +534,20 @@ class QuantizedLayer:
         self.out = torch.empty((w.n, w.d), dtype=dt, device=device)
 
     def forward(self, X, stream=None):
-        _ptr(X, "X", self.out.dtype, self.out.shape, _device_of(self.out))
-        moe.moe_route(self.cfg, X, self.Wg, self.logit_bias, self.sel_bias, self.route, self.ws,
-                      stream)
-        moe_dispatch_i8(self.dispatch_cfg, X, self.route, self.Xq, self.xs, self.starts,
-                        self.counts, stream)
-        # the products share the routing workspace's error word
-        moe_gemm_i8(self.up, self.Xq, self.xs, self.starts, self.counts, self.W1, self.s1,
-                    self.W3, self.s3, self.H, self.ws, stream)
-        moe_quantize_rows(self.H, self.Hq, self.hs, self.starts, self.counts, stream)
-        moe_gemm_i8(self.down, self.Hq, self.hs, self.starts, self.counts, self.W2, self.s2,
-                    None, None, self.Y, self.ws, stream)
-        moe.moe_combine(self.cfg, self.Y, self.route, self.out, stream)
+        dev = _device_of(self.out)
+        _ptr(X, "X", self.out.dtype, self.out.shape, dev)
+        with _on(dev, stream):
+            moe.moe_route(self.cfg, X, self.Wg, self.logit_bias, self.sel_bias, self.route,
+                          self.ws, stream)
+            moe_dispatch_i8(self.dispatch_cfg, X, self.route, self.Xq, self.xs, self.starts,
+                            self.counts, stream)
+            # the products share the routing workspace's error word
+            moe_gemm_i8(self.up, self.Xq, self.xs, self.starts, self.counts, self.W1, self.s1,
+                        self.W3, self.s3, self.H, self.ws, stream)
+            moe_quantize_rows(self.H, self.Hq, self.hs, self.starts, self.counts, stream)
+            moe_gemm_i8(self.down, self.Hq, self.hs, self.starts, self.counts, self.W2, self.s2,
+                        None, None, self.Y, self.ws, stream)
+            moe.moe_combine(self.cfg, self.Y, self.route, self.out, stream)
         return self.out
 
 
@@ -563,9 +584,10 @@ class Block:
     def forward(self, x, stream=None, train=False):
         """(out, h_next). With train, the layer keeps what its backward needs."""
         self.x = x
-        moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)
-        run = self.layer.forward_train if train else self.layer.forward
-        return self._tail(run(self.h, stream=stream), stream)
+        with _on(_device_of(self.out), stream):
+            moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)
+            run = self.layer.forward_train if train else self.layer.forward
+            return self._tail(run(self.h, stream=stream), stream)
 
     def forward_train(self, x, stream=None):
         return self.forward(x, stream, train=True)
@@ -583,12 +605,17 @@ class Block:
                 g["d" + k] = None if t is None else torch.empty_strided(
                     t.shape, t.stride(), dtype=t.dtype, device=t.device)
             self._nws = norm_workspace(self.cfg, self.out.device)
-            g["layer"] = self.layer.grads()
+            with _on(_device_of(self.out), None):
+                g["layer"] = self.layer.grads()
             self._g = g
         return self._g
 
     def backward_train(self, dout, dh_next=None, stream=None):
         """Gradients of <dout, out> + <dh_next, h_next> after forward_train()."""
+        with _on(_device_of(self.out), stream):
+            return self._backward(dout, dh_next, stream)
+
+    def _backward(self, dout, dh_next, stream):
         p, g = self.p, self.grads()
         r_post = self.r_post if p.get("w_post") is not None else None
         r_next = self.r_next if p.get("w_next") is not None else None
@@ -606,15 +633,17 @@ class Block:
     def clip_grads(self, max_norm: float, stream=None):
         """Scales the parameters' gradients in place so that their global norm
         is at most max_norm; returns the device tensor [norm, factor]."""
-        if not hasattr(self, "_clip"):
-            g = self.grads()
-            own = [g[k] for k in ("dw_pre", "dw_post", "dgate", "dw_next")]
-            own += [t for k, t in g["layer"].items() if k not in ("dX", "dL")]
-            own = [t for t in own if t is not None]
-            # what lies between the rows of a strided gate's gradient is no gradient
-            glist = grad_list([r for t in own for r in ([t] if t.is_contiguous() else t.unbind())])
-            self._clip = (glist, torch.empty(2, dtype=torch.float32, device=self.out.device),
-                          grad_workspace(glist, self.out.device))
-        glist, norm, ws = self._clip
-        moe_grad_clip(glist, max_norm, norm, ws, stream)
-        return norm
+        with _on(_device_of(self.out), stream):
+            if not hasattr(self, "_clip"):
+                g = self.grads()
+                own = [g[k] for k in ("dw_pre", "dw_post", "dgate", "dw_next")]
+                own += [t for k, t in g["layer"].items() if k not in ("dX", "dL")]
+                own = [t for t in own if t is not None]
+                # what lies between the rows of a strided gate's gradient is no gradient
+                glist = grad_list([r for t in own
+                                   for r in ([t] if t.is_contiguous() else t.unbind())])
+                self._clip = (glist, torch.empty(2, dtype=torch.float32, device=self.out.device),
+                              grad_workspace(glist, self.out.device))
+            glist, norm, ws = self._clip
+            moe_grad_clip(glist, max_norm, norm, ws, stream)
+            return norm

@@ -73,6 +73,52 @@ def calls(monkeypatch):
 
 
 W = wl.SMALL[3].replace(name="host", n=40)
+SERVE = ["moe_route", "moe_dispatch_i8", "moe_gemm_i8", "moe_quantize_rows", "moe_gemm_i8",
+         "moe_combine"]
+TAIL = "moe_residual_norm_forward"
+
+
+class Stream:
+    def __init__(self, dev=HERE):
+        self.device = types.SimpleNamespace(index=dev)
+
+
+def params():
+    return {k: torch.ones(W.d) for k in ("w_pre", "w_post", "w_next")}
+
+
+def test_quantized_layer_runs_on_its_tensors_device(calls):
+    inp = wl.make_inputs(W)
+    q = block.QuantizedLayer(W, inp, "cpu")
+    assert "moe.workspace" in calls.names() and "moe_quantize_rows" in calls.names()
+    assert all(c[1] == HERE for c in calls.log)
+    calls.log.clear()
+    q.forward(inp["X"])
+    assert calls.names() == SERVE and {c[1:] for c in calls.log} == {(HERE, "the tensors'")}
+    assert calls.device == 0
+    calls.log.clear()
+    s = Stream()
+    q.forward(inp["X"], s)
+    assert {c[1:] for c in calls.log} == {(HERE, s)}
+
+
+def test_block_runs_on_its_tensors_device(calls):
+    inp = wl.make_inputs(W)
+    for s in (None, Stream()):
+        calls.log.clear()
+        b = block.Block(moe.Layer(W, inp, "cpu"), params())
+        calls.log.clear()  # (a layer is made on the current device, as ever)
+        x = inp["X"]
+        out, _ = b.forward(x, stream=s)
+        out, _ = b.forward_train(x, stream=s)
+        b.backward_train(out, out, stream=s)
+        b.clip_grads(1.0, stream=s)
+        want = ["moe_norm_forward", "moe_layer_forward", TAIL, "moe_norm_forward",
+                "backward_workspace", "moe_layer_forward_train", TAIL,
+                "moe_residual_norm_backward", "moe_layer_backward_train", "moe_norm_backward",
+                "grad_workspace", "moe_grad_clip"]
+        assert calls.names() == want
+        assert {c[1:] for c in calls.log} == {(HERE, s or "the tensors'")}
 
 
 def test_quantized_layer_refuses_before_the_first_step(calls):
@@ -91,3 +137,15 @@ def test_quantized_layer_refuses_before_the_first_step(calls):
                  ("Wg", None)):
         with pytest.raises((TypeError, ValueError)):
             block.QuantizedLayer(W, {**inp, k: t}, "cpu")
+
+
+def test_streams_of_another_device_are_refused(calls):
+    inp = wl.make_inputs(W)
+    b = block.Block(moe.Layer(W, inp, "cpu"), params())
+    q = block.QuantizedLayer(W, inp, "cpu")
+    calls.log.clear()
+    for call in (lambda: b.forward(inp["X"], Stream(0)), lambda: b.clip_grads(1.0, Stream(0)),
+                 lambda: q.forward(inp["X"], Stream(0))):
+        with pytest.raises(ValueError):
+            call()
+    assert not calls.log
