@@ -572,6 +572,11 @@ class Block:
         self.h_next = torch.empty((w.n, w.d), **x) if params.get("w_next") is not None else None
         self.r_pre, self.r_post, self.r_next = (torch.empty(w.n, **f) for _ in range(3))
         self._g = None
+        self._trained = False  # the last forward was forward_train()
+
+    def _trains(self):
+        if not hasattr(self.layer, "backward_train"):
+            raise TypeError(f"a {type(self.layer).__name__} has no backward pass")
 
     def _tail(self, y, stream):
         p = self.p
@@ -583,11 +588,14 @@ class Block:
 
     def forward(self, x, stream=None, train=False):
         """(out, h_next). With train, the layer keeps what its backward needs."""
+        self._trained = False
         self.x = x
         with _on(_device_of(self.out), stream):
             moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)
             run = self.layer.forward_train if train else self.layer.forward
-            return self._tail(run(self.h, stream=stream), stream)
+            res = self._tail(run(self.h, stream=stream), stream)
+        self._trained = train
+        return res
 
     def forward_train(self, x, stream=None):
         return self.forward(x, stream, train=True)
@@ -595,8 +603,7 @@ class Block:
     def grads(self):
         """Gradient buffers (allocated once): "dx", the norms' and the gate's,
         and the layer's own."""
-        if not hasattr(self.layer, "backward_train"):
-            raise TypeError(f"a {type(self.layer).__name__} has no backward pass")
+        self._trains()
         if self._g is None:
             p, g = self.p, {"dx": torch.empty_like(self.out), "dy": torch.empty_like(self.out),
                             "dw_pre": torch.empty_like(self.p["w_pre"])}
@@ -612,6 +619,10 @@ class Block:
 
     def backward_train(self, dout, dh_next=None, stream=None):
         """Gradients of <dout, out> + <dh_next, h_next> after forward_train()."""
+        self._trains()
+        if not self._trained:
+            raise RuntimeError("backward_train() goes back through forward_train(): the last "
+                               "forward of this block was none")
         with _on(_device_of(self.out), stream):
             return self._backward(dout, dh_next, stream)
 

@@ -149,3 +149,27 @@ def test_streams_of_another_device_are_refused(calls):
         with pytest.raises(ValueError):
             call()
     assert not calls.log
+
+
+def test_backward_needs_the_forward_that_kept_its_inputs(calls):
+    """After forward(), the layer's saved activations are of an earlier step, or none."""
+    inp = wl.make_inputs(W)
+    b = block.Block(moe.Layer(W, inp, "cpu"), params())
+    x = inp["X"]
+    with pytest.raises(RuntimeError, match="forward_train"):
+        b.backward_train(x, x)
+    b.forward(x)
+    with pytest.raises(RuntimeError, match="forward_train"):
+        b.backward_train(x, x)
+    b.forward_train(x)
+    b.backward_train(x, x)
+    b.backward_train(x, x)  # again, with other gradients
+    b.forward(x)
+    with pytest.raises(RuntimeError, match="forward_train"):
+        b.backward_train(x, x)
+    # a forward that fails leaves nothing to go back through
+    b.forward_train(x)
+    with pytest.raises(ValueError):
+        b.forward_train(x[:-1])
+    with pytest.raises(RuntimeError, match="forward_train"):
+        b.backward_train(x, x)
