@@ -588,6 +588,8 @@ class Block:
 
     def forward(self, x, stream=None, train=False):
         """(out, h_next). With train, the layer keeps what its backward needs."""
+        if train:
+            self._trains()
         self._trained = False
         self.x = x
         with _on(_device_of(self.out), stream):
@@ -618,7 +620,8 @@ class Block:
         return self._g
 
     def backward_train(self, dout, dh_next=None, stream=None):
-        """Gradients of <dout, out> + <dh_next, h_next> after forward_train()."""
+        """Gradients of <dout, out> + <dh_next, h_next>, when the block's last forward
+        was forward_train(). (A graph's replay is no call of this object's.)"""
         self._trains()
         if not self._trained:
             raise RuntimeError("backward_train() goes back through forward_train(): the last "

@@ -173,3 +173,14 @@ def test_backward_needs_the_forward_that_kept_its_inputs(calls):
         b.forward_train(x[:-1])
     with pytest.raises(RuntimeError, match="forward_train"):
         b.backward_train(x, x)
+
+
+def test_training_of_8_bit_experts_is_refused(calls):
+    inp = wl.make_inputs(W)
+    b = block.Block(block.QuantizedLayer(W, inp, "cpu"), params())
+    calls.log.clear()
+    with pytest.raises(TypeError, match="no backward pass"):
+        b.forward_train(inp["X"])
+    with pytest.raises(TypeError, match="no backward pass"):
+        b.clip_grads(1.0)
+    assert not calls.log
