@@ -559,16 +559,27 @@ class Block:
         out = a x + b gate * norm(y; w_post)  residual norm
         h_next = norm(out; w_next)            the next block's pre-norm, fused
 
-    params: fp32 "w_pre" [d], and optionally "w_post" [d], "gate" (rows of the
-    layer's dtype, see norm_config) and "w_next" [d]."""
+    params: optionally fp32 "w_pre" [d], "w_post" [d], "gate" (rows of the layer's
+    dtype, see norm_config) and "w_next" [d]. A block without "w_pre" has no
+    pre-norm of its own: it takes h beside x, as the block before it left it, and
+    its backward pass gives "dx" (along the residual) and "dh" for that block:
+
+        out, h = one.forward_train(x)              # one has "w_next"
+        out, _ = two.forward_train(out, h=h)       # two has no "w_pre"
+        g = two.backward_train(dout)
+        g = one.backward_train(g["dx"], g["dh"])   # "dw_next" among its gradients
+
+    A block keeps x and h themselves, not copies, until its backward pass."""
 
     def __init__(self, layer, params: dict, eps: float = 1e-6, **norm):
         self.layer, self.p = layer, params
         w = layer.w
         self.cfg = norm_config(w.n, w.d, w.torch_dtype, eps, **norm)
-        x = dict(dtype=w.torch_dtype, device=params["w_pre"].device)
+        x = dict(dtype=w.torch_dtype, device=layer.out.device)
         f = dict(dtype=torch.float32, device=x["device"])
-        self.h, self.out = torch.empty((w.n, w.d), **x), torch.empty((w.n, w.d), **x)
+        self.pre = params.get("w_pre") is not None
+        self.h = torch.empty((w.n, w.d), **x) if self.pre else None
+        self.out = torch.empty((w.n, w.d), **x)
         self.h_next = torch.empty((w.n, w.d), **x) if params.get("w_next") is not None else None
         self.r_pre, self.r_post, self.r_next = (torch.empty(w.n, **f) for _ in range(3))
         self._g = None
@@ -586,36 +597,44 @@ class Block:
                                   self.r_next if p.get("w_next") is not None else None, stream)
         return self.out, self.h_next
 
-    def forward(self, x, stream=None, train=False):
+    def forward(self, x, stream=None, train=False, h=None):
         """(out, h_next). With train, the layer keeps what its backward needs."""
         if train:
             self._trains()
         self._trained = False
+        if self.pre and h is not None:
+            raise ValueError("h is given to a block that has a pre-norm of its own (w_pre)")
+        dev = _device_of(self.out)
+        if not self.pre:  # (the layer's binding checks no shapes)
+            for name, t in (("x", x), ("h", h)):
+                _ptr(t, name, self.out.dtype, self.out.shape, dev)
+            self.h = h
         self.x = x
-        with _on(_device_of(self.out), stream):
-            moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)
+        with _on(dev, stream):
+            if self.pre:
+                moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)
             run = self.layer.forward_train if train else self.layer.forward
             res = self._tail(run(self.h, stream=stream), stream)
         self._trained = train
         return res
 
-    def forward_train(self, x, stream=None):
-        return self.forward(x, stream, train=True)
+    def forward_train(self, x, stream=None, h=None):
+        return self.forward(x, stream, train=True, h=h)
 
     def grads(self):
-        """Gradient buffers (allocated once): "dx", the norms' and the gate's,
-        and the layer's own."""
+        """Gradient buffers (allocated once): "dx" ("dh" too, without a pre-norm), the
+        norms' and the gate's, and the layer's own."""
         self._trains()
         if self._g is None:
-            p, g = self.p, {"dx": torch.empty_like(self.out), "dy": torch.empty_like(self.out),
-                            "dw_pre": torch.empty_like(self.p["w_pre"])}
-            for k in ("w_post", "gate", "w_next"):
+            p, g = self.p, {"dx": torch.empty_like(self.out), "dy": torch.empty_like(self.out)}
+            for k in ("w_pre", "w_post", "gate", "w_next"):
                 t = p.get(k)  # (a gate's gradient has the gate's stride between rows)
                 g["d" + k] = None if t is None else torch.empty_strided(
                     t.shape, t.stride(), dtype=t.dtype, device=t.device)
             self._nws = norm_workspace(self.cfg, self.out.device)
             with _on(_device_of(self.out), None):
                 g["layer"] = self.layer.grads()
+            g["dh"] = None if self.pre else g["layer"]["dX"]
             self._g = g
         return self._g
 
@@ -640,8 +659,9 @@ class Block:
                                    r_next, g["dx"], g["dy"], g["dw_post"], g["dgate"],
                                    g["dw_next"], self._nws, stream)
         lg = self.layer.backward_train(g["dy"], X=self.h, stream=stream)
-        moe_norm_backward(self.cfg, g["dx"], lg["dX"], self.x, p["w_pre"], self.r_pre, g["dx"],
-                          g["dw_pre"], self._nws, stream)
+        if self.pre:
+            moe_norm_backward(self.cfg, g["dx"], lg["dX"], self.x, p["w_pre"], self.r_pre,
+                              g["dx"], g["dw_pre"], self._nws, stream)
         return g
 
     def clip_grads(self, max_norm: float, stream=None):

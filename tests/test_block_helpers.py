@@ -184,3 +184,25 @@ def test_training_of_8_bit_experts_is_refused(calls):
     with pytest.raises(TypeError, match="no backward pass"):
         b.clip_grads(1.0)
     assert not calls.log
+
+
+def test_a_block_that_takes_its_normed_input(calls):
+    inp = wl.make_inputs(W)
+    p = {k: torch.ones(W.d) for k in ("w_post", "w_next")}
+    b = block.Block(moe.Layer(W, inp, "cpu"), p)
+    own = block.Block(moe.Layer(W, inp, "cpu"), {**p, "w_pre": torch.ones(W.d)})
+    x, h = inp["X"], inp["X"].clone()
+    calls.log.clear()
+    for bad, error in (((x, None), ValueError), ((x, h[:-1]), ValueError),
+                       ((x[:-1], h), ValueError), ((x.float(), h), TypeError),
+                       ((x, h.float()), TypeError)):
+        with pytest.raises(error):
+            b.forward_train(bad[0], h=bad[1])
+    with pytest.raises(ValueError):  # which norm?
+        own.forward(x, h=h)
+    assert not calls.log
+    out, _ = b.forward_train(x, h=h)
+    g = b.backward_train(out, out)
+    assert calls.names() == ["backward_workspace", "moe_layer_forward_train", TAIL,
+                             "moe_residual_norm_backward", "moe_layer_backward_train"]
+    assert g["dh"] is g["layer"]["dX"] and g["dw_pre"] is None
