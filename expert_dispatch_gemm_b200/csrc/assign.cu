@@ -266,9 +266,8 @@ static size_t select_ec_smem(int /*nt*/, int k) {
 template <int NT>
 static cudaError_t launch_select_ec_t(const SelectEcArgs& a, cudaStream_t s) {
   const size_t bytes = select_ec_smem(NT, a.k);
-  cudaError_t err = cudaFuncSetAttribute(select_ec_kernel<NT>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)bytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t err = allow_all_smem(select_ec_kernel<NT>, done);
   if (err != cudaSuccess) return err;
   return launch_pdl(select_ec_kernel<NT>, a.E, NT, bytes, s, a);
 }
@@ -353,8 +352,8 @@ __global__ void __launch_bounds__(256) ec_finish_kernel(EcFinishArgs a) {
 // (select_ec_kernel's block 0 has zeroed hist and the aux slots)
 cudaError_t launch_ec_finish(const EcFinishArgs& a, cudaStream_t s) {
   const size_t bytes = (size_t)a.E * 33 * 8;
-  cudaError_t e = cudaFuncSetAttribute(ec_finish_kernel,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_all_smem(ec_finish_kernel, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(ec_finish_kernel, ceil_div(a.n, 32), 256, bytes, s, a);
 }
@@ -574,8 +573,8 @@ cudaError_t launch_tc_assign(const TcAssignArgs& a, cudaStream_t s) {
   e = launch_pdl(tc_scan_kernel, 1, kScanThreads, 0, s, a);
   if (e != cudaSuccess) return e;
   const size_t bytes = (size_t)(2 * (kTokBlock / 32) + 1) * a.E * 4;
-  e = cudaFuncSetAttribute(tc_scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)bytes);
+  static std::atomic<uint64_t> done{0};
+  e = allow_all_smem(tc_scatter_kernel, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(tc_scatter_kernel, a.tok_blocks, kTokBlock, bytes, s, a);
 }

@@ -399,9 +399,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwd p) {
 // Threads a worker: 8 columns each up to d = 8192, 16 above.
 int norm_threads(int d) { return ((d <= 8192 ? (d + 7) / 8 : (d + 15) / 16) + 31) / 32 * 32; }
 // shared memory for one worker's ring where `per_sm` of them share an SM
-constexpr size_t ring_budget(int per_sm) { return (size_t)(224 * 1024) / per_sm - 2048; }
-// the most that a launch of any width takes
-constexpr size_t kMostSmem = ring_budget(1);
+size_t ring_budget(int per_sm) { return (size_t)(224 * 1024) / per_sm - 2048; }
 
 int fwd_workers_per_sm(int d) {
   const int k = 1024 / norm_threads(d);
@@ -413,7 +411,7 @@ cudaError_t run_fwd(const NormFwd& p, size_t smem, cudaStream_t s) {
   auto kern = norm_fwd_kernel<T, VEC, EPT, STAGED>;
   if (smem > 32 * 1024) {  // (48 KB with the static part need no leave)
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(kern, kMostSmem, done);
+    const cudaError_t e = allow_all_smem(kern, done);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, dim3(p.workers), dim3(norm_threads(p.d)), smem, s, p);
@@ -909,7 +907,7 @@ cudaError_t run_bwd(const NormBwd& p, int groups, size_t smem, cudaStream_t s) {
   auto kern = norm_bwd_kernel<T, VEC, EPT, STAGED, MAXT, ALL>;
   if (smem > 32 * 1024) {  // (48 KB with the static part need no leave)
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(kern, kMostSmem, done);
+    const cudaError_t e = allow_all_smem(kern, done);
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(kern, dim3(p.blocks), dim3(norm_threads(p.d), groups), smem, s, p);

@@ -213,8 +213,8 @@ cudaError_t launch_gather(const GatherArgs& a, cudaStream_t s) {
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaDeviceGetAttribute(&max_smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
-  cudaError_t e = cudaFuncSetAttribute(gather_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_all_smem(gather_kernel, done);
   if (e != cudaSuccess) return e;
   int per_sm = (int)(max_smem / (smem + 1024));
   per_sm = per_sm < 1 ? 1 : per_sm > 4 ? 4 : per_sm;

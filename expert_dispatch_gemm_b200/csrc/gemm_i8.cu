@@ -1077,7 +1077,7 @@ constexpr size_t smem_bytes(int ring) {
 template <auto kern, class... Args>
 cudaError_t launch_i8(int pairs, size_t bytes, cudaStream_t s, const Args&... args) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(kern, bytes, done);
+  const cudaError_t e = allow_all_smem(kern, done);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(2 * pairs), dim3(kThreads), bytes, s, args...);
 }
@@ -1086,7 +1086,7 @@ cudaError_t launch_i8(int pairs, size_t bytes, cudaStream_t s, const Args&... ar
 template <auto kern, class... Args>
 cudaError_t launch_split(int tiles, int parts, size_t bytes, cudaStream_t s, const Args&... args) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(kern, bytes, done);
+  const cudaError_t e = allow_all_smem(kern, done);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * parts * tiles);
