@@ -25,16 +25,18 @@
 // to be bound by HBM, which leaves about 20 instructions an element. So
 // - a block (worker) owns a contiguous range of rows, and a thread the same 8
 //   columns (16 above d = 8192) of each: weights, the gate's product with them
-//   and the sums over tokens stay in its registers;
+//   and the sums over tokens stay in its registers (of 16 columns, in the backward,
+//   as far as 64 hold them: 500 to 700 bytes a thread are spilled and read again);
 // - arithmetic is on packed fp32 pairs;
 // - the next rows' chunks come into shared memory by cp.async while a row is
 //   computed; each thread reads back only what it copied itself, so no barrier
 //   guards the ring, and the only barriers are those of the row sums.
 // On a B200, replayed from a graph: forward, n 8192, d 7168 bf16, 81 to 83 us
 // (5.7 TB/s, 87 to 89% of a copy's rate; without the ring and the packed pairs
-// 112); backward, n 16384, d 2048 bf16, one gate row, 70 to 72 us (5.6 TB/s, 86 to
-// 88%), n 8192, d 7168 151 us (71%: one worker an SM, whose warps wait for each
-// other at every row).
+// 112); backward, n 16384, d 2048 bf16, one gate row, 70 to 73 us (5.6 TB/s, 84 to
+// 88%), n 8192, d 7168 153 to 157 us (69 to 70%: one worker an SM, whose warps wait
+// for each other at every row), n 2048, d 16384 165 us (37%: spills); the pre-norm's
+// own, n 8192, d 7168, 222 us (32%: the general instance below, which spills too).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -931,6 +933,9 @@ cudaError_t launch_bwd(NormBwd& p, int groups, int bytes, cudaStream_t s) {
   const int deep = (p.n + p.workers - 1) / p.workers;
   p.stages = fit > kMaxStages ? kMaxStages : (int)fit;
   if (p.stages > deep) p.stages = deep;
+  // Where no stage fits beside the workers that the split gives a block, the rows go
+  // through single loads, whatever their alignment: fp32 with a gate row for each
+  // token, n 4096, d 4096 189 us against 103 at d 3840 and 144 at d 4160, where one fits.
   const bool staged = bytes >= 4 && p.stages >= 1 && ends + sums <= budget;
   if (!staged) p.stages = 1;
   const size_t ring = staged ? p.stages * p.slots * row : 0;

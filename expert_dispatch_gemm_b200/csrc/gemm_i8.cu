@@ -29,8 +29,8 @@
 //   stage, u and v into two accumulators that meet in one epilogue thread.
 //     warp 0 producer, 1 / 2 issuers, 4-19 epilogue
 // On a B200 (8-bit rate: twice the measured bf16 rate, 3.3 POP/s; uniform random
-// bytes): k 14336, 1,280 rows a group 3.0 POP/s (91%); SwiGLU, k 4096, 802 us for
-// 10,240 rows and 14,336 units (90%; its epilogue is not overlapped, 70 us of it);
+// bytes): k 14336, 1,280 rows a group 3.0 POP/s (91%); SwiGLU, k 4096, 813 to 827 us
+// for 10,240 rows and 14,336 units (88 to 89%; its epilogue is not overlapped);
 // k 1024, 2,048 rows a group, 262 us for 131,072 rows and 2,048 channels (64%: the
 // SMs' path to L2, see the epilogue); 16 rows a group of 32, k 7168, SwiGLU 2048,
 // 148 to 154 us (94 to 97% of the HBM rate).
@@ -762,7 +762,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // distributed shared memory, adds what it received to its own, and writes. One
 // row, weights from HBM: k 2048, 7,168 channels (28 tiles, 2 parts) 9.3 us, unsplit
 // 10.7; k 7168, 2,048 channels (8 tiles, 4 parts) 11.7 us, unsplit 25.3. The
-// smallest product of all takes 5.6.
+// smallest product of all takes 5.6. (The tiles are the host's bound from the rows of
+// the buffers. A layer's buffers have room for 127 rows of padding an expert, which
+// keeps its products above the limit; calls with one or a few groups come here.)
 // ---------------------------------------------------------------------------
 constexpr int kSplitRing = 192 * 1024;
 constexpr int kSplitStages = 6;  // of 32 KB; SwiGLU 4 of 48 KB
