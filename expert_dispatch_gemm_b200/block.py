@@ -314,7 +314,8 @@ def moe_residual_norm_backward(cfg: MoeNormConfig, dout, dh, out, y, w_post, gat
 class GradList:
     """The gradients of one moe_grad_norm / moe_grad_clip call, and where the
     clipped copies go (None: in place). Holds the tensors; their addresses are
-    taken here, once."""
+    taken here, once. Outputs may not overlap, so a tensor that is listed twice needs
+    two outputs of its own, for moe_grad_norm too, which leaves them alone."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -666,7 +667,8 @@ class Block:
 
     def clip_grads(self, max_norm: float, stream=None):
         """Scales the parameters' gradients in place so that their global norm
-        is at most max_norm; returns the device tensor [norm, factor]."""
+        is at most max_norm; returns the device tensor [norm, factor], the same
+        one at each call."""
         with _on(_device_of(self.out), stream):
             if not hasattr(self, "_clip"):
                 g = self.grads()

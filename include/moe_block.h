@@ -148,9 +148,10 @@ MOE_API moe_status moe_grad_clip(const moe_grad_tensor* tensors, int count, floa
 
 /* Symmetric quantisation, row by row: scale[r] = max_j |x[r,j]| / 127 in fp32,
  * q[r,j] = x[r,j] / scale[r] rounded to the nearest integer, ties to even
- * (decided on the exact quotient). A row of zeros gets scale 0 and zeros; a
- * row with an infinity or a NaN gets scale NaN and zeros, so that every
- * product with it is NaN. x [rows, cols] of `dtype` (cols >= 1), q [rows, cols] int8,
+ * (decided on the exact quotient), at most 127. A row of zeros, or one so small
+ * that its scale rounds to 0 (max |x| up to 63 * 2^-149), gets scale 0 and
+ * zeros; a row with an infinity or a NaN gets scale NaN and zeros, so that
+ * every product with it is NaN. x [rows, cols] of `dtype` (cols >= 1), q [rows, cols] int8,
  * scale [rows] fp32. With starts / counts [groups] (both or neither), only
  * rows starts[g] .. starts[g] + counts[g] - 1 of each group are read and
  * written (groups in ascending order of their rows, inside [0, rows)); the
