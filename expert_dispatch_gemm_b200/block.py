@@ -609,8 +609,15 @@ class Block:
         if not self.pre:  # (the layer's binding checks no shapes)
             for name, t in (("x", x), ("h", h)):
                 _ptr(t, name, self.out.dtype, self.out.shape, dev)
-            self.h = h
+        if train:  # (the tail of this call writes them)
+            mine = [t.data_ptr() for t in (self.out, self.h_next) if t is not None]
+            for name, t in (("x", x), ("h", h)):
+                if t is not None and t.numel() and t.data_ptr() in mine:
+                    raise ValueError(f"{name} is an output of this block: it would be overwritten "
+                                     "before the backward pass reads it")
         self.x = x
+        if not self.pre:
+            self.h = h
         with _on(dev, stream):
             if self.pre:
                 moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)

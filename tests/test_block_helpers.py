@@ -206,3 +206,22 @@ def test_a_block_that_takes_its_normed_input(calls):
     assert calls.names() == ["backward_workspace", "moe_layer_forward_train", TAIL,
                              "moe_residual_norm_backward", "moe_layer_backward_train"]
     assert g["dh"] is g["layer"]["dX"] and g["dw_pre"] is None
+
+
+def test_training_on_the_blocks_own_outputs_is_refused(calls):
+    """They are overwritten by the forward that should be gone back through; without
+    a backward pass a block may take them."""
+    inp = wl.make_inputs(W)
+    b = block.Block(moe.Layer(W, inp, "cpu"), params())
+    two = block.Block(moe.Layer(W, inp, "cpu"), {"w_next": torch.ones(W.d)})
+    x = inp["X"]
+    out, h = b.forward_train(x)
+    out2, h2 = two.forward_train(out, h=h)
+    calls.log.clear()
+    for call in (lambda: b.forward_train(out), lambda: b.forward_train(h),
+                 lambda: two.forward_train(out2, h=h), lambda: two.forward_train(out, h=h2)):
+        with pytest.raises(ValueError, match="overwritten"):
+            call()
+    assert not calls.log
+    b.forward(out)
+    two.forward(out2, h=h2)
