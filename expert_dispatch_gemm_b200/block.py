@@ -570,7 +570,8 @@ class Block:
         g = two.backward_train(dout)
         g = one.backward_train(g["dx"], g["dh"])   # "dw_next" among its gradients
 
-    A block keeps x and h themselves, not copies, until its backward pass."""
+    A block keeps x and h themselves, not copies, until its backward pass; a layer
+    keeps one forward's activations, so blocks that train have a layer each."""
 
     def __init__(self, layer, params: dict, eps: float = 1e-6, **norm):
         self.layer, self.p = layer, params
@@ -618,6 +619,7 @@ class Block:
         self.x = x
         if not self.pre:
             self.h = h
+        self.layer._in_block = self  # whose forward its buffers hold
         with _on(dev, stream):
             if self.pre:
                 moe_norm_forward(self.cfg, x, self.p["w_pre"], self.h, self.r_pre, stream)
@@ -653,6 +655,9 @@ class Block:
         if not self._trained:
             raise RuntimeError("backward_train() goes back through forward_train(): the last "
                                "forward of this block was none")
+        if self.layer._in_block is not self:
+            raise RuntimeError("another block has run this layer since: its activations are of "
+                               "that forward")
         with _on(_device_of(self.out), stream):
             return self._backward(dout, dh_next, stream)
 

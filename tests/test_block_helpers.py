@@ -225,3 +225,21 @@ def test_training_on_the_blocks_own_outputs_is_refused(calls):
     assert not calls.log
     b.forward(out)
     two.forward(out2, h=h2)
+
+
+def test_a_layer_in_two_blocks_goes_back_through_the_last_one_only(calls):
+    """The layer keeps one forward's activations: the other block's are gone."""
+    inp = wl.make_inputs(W)
+    layer = moe.Layer(W, inp, "cpu")
+    one, two = block.Block(layer, params()), block.Block(layer, params())
+    x = inp["X"]
+    one.forward_train(x)
+    two.forward_train(x)
+    two.backward_train(x, x)
+    with pytest.raises(RuntimeError, match="another block"):
+        one.backward_train(x, x)
+    one.forward_train(x)
+    one.backward_train(x, x)
+    two.forward(x)  # serving through the same layer overwrites them too
+    with pytest.raises(RuntimeError, match="another block"):
+        one.backward_train(x, x)
